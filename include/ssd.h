@@ -374,11 +374,196 @@ ssd_status ssd_scan_bwd_complex(const float *x, const float *dt, const float *A,
                                 size_t workspace_bytes, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The rest of a mixer block, around its matrix products: the short convolution
+ * and the Mamba-1 scan on packed prompts and on single tokens, with gradients,
+ * and the norms before and after the block.
+ *
+ * Packed sequences.  The tokens of all sequences of a call lie one after another
+ * in `tokens` rows; sequence i holds rows cu_seqlens[i] .. cu_seqlens[i+1]-1
+ * (int32, device memory, nseq + 1 entries, not decreasing; a sequence may be
+ * empty).  Rows of no sequence are not read, and forward outputs leave them as
+ * they were; gradients are zero there.  A sequence whose bounds do not lie in
+ * 0 .. tokens is skipped, and the next ssd_get_device_status reports
+ * SSD_ERR_INVALID_ARG.
+ *
+ * State slots.  A cache holds nslots states; sequence (or batch row) i uses state
+ * slots[i] (int32, device memory), or state i when slots is NULL.  A prompt starts
+ * from its slot's state where has_init[i] != 0 (bytes, device memory; NULL: no
+ * prompt does) and from zero otherwise, and leaves its end state there; an empty
+ * prompt leaves its slot as it was.  A negative slot means none: a prompt then
+ * starts from zero and its end state is dropped, a batch row of a single-token
+ * call is skipped and its output row left as it was.  The same goes for a slot
+ * that is not below nslots or that an earlier entry of the same call names (two
+ * sequences cannot share a state), and the next ssd_get_device_status reports
+ * SSD_ERR_INVALID_ARG.
+ *
+ * Row strides (in elements) may exceed a row's width, so that slices of a
+ * projection's output go in as they are; such inputs need their element's
+ * alignment only (16-byte aligned rows are read wider).  Inner strides are 1.
+ * All other tensors are contiguous and 16-byte aligned.  Arithmetic is float32
+ * whatever io_dtype, rounded once on output.  Nothing is allocated; a workspace
+ * needs no initialisation and serves one call at a time.
+ */
+
+/*
+ * The convolution of ssd_conv1d_xbc on packed sequences.
+ *  xbc  [tokens, x_channels + 2 bc_channels] io_dtype, row stride xbc_stride
+ *  weight, bias: as ssd_conv1d_xbc;  x_out, B_out, C_out [tokens, ...] contiguous
+ *  conv_state [nslots, channels, width-1] io_dtype (the last width-1 inputs), or
+ *       NULL: every sequence starts from zero
+ * One launch.
+ */
+ssd_status ssd_conv1d_varlen(const void *xbc, long long xbc_stride, const float *weight,
+                             const float *bias, const int *cu_seqlens, void *conv_state,
+                             const int *slots, const unsigned char *has_init, void *x_out,
+                             void *B_out, void *C_out, ssd_dtype io_dtype, int tokens, int nseq,
+                             int nslots, int x_channels, int bc_channels, int width, int silu,
+                             void *stream);
+
+/* One token per sequence: xbc [batch, channels]; conv_state is read and moved on
+ * in place.  batch <= 65535. */
+ssd_status ssd_conv1d_update(void *conv_state, const int *slots, const void *xbc,
+                             long long xbc_stride, const float *weight, const float *bias,
+                             void *x_out, void *B_out, void *C_out, ssd_dtype io_dtype, int batch,
+                             int nslots, int x_channels, int bc_channels, int width, int silu,
+                             void *stream);
+
+/*
+ * Gradient of ssd_conv1d_varlen without states (every sequence from zero): from
+ * dx_out, dB_out, dC_out (contiguous, as the outputs) dxbc [tokens, channels]
+ * io_dtype, contiguous, and dweight, dbias (or NULL) float32, summed in a fixed
+ * order.  The inputs are those of the forward; nothing else is kept.  Two launches.
+ */
+size_t ssd_conv1d_bwd_workspace_size(int tokens, int channels, int width);
+ssd_status ssd_conv1d_bwd(const void *xbc, long long xbc_stride, const float *weight,
+                          const float *bias, const int *cu_seqlens, const void *dx_out,
+                          const void *dB_out, const void *dC_out, void *dxbc, float *dweight,
+                          float *dbias, ssd_dtype io_dtype, int tokens, int nseq, int x_channels,
+                          int bc_channels, int width, int silu, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * What every call of the gated Mamba-1 scan takes:
+ *
+ *   delta = softplus(dt + dt_bias), or dt + dt_bias when softplus is 0
+ *   h_t[n] = exp(delta_t A[n]) h_{t-1}[n] + delta_t x_t B_t[n]
+ *   y_t = (sum_n C_t[n] h_t[n] + D x_t) silu(z_t)      for each channel
+ *
+ *  x, dt, z  [rows, channels] io_dtype with row strides (z NULL: no gate; rows are
+ *            tokens, or the batch of a single-token call)
+ *  B, C      [rows, ngroups, dstate] io_dtype with row strides; channel d reads
+ *            group d / (channels / ngroups)
+ *  A [channels, dstate], D and dt_bias [channels] (or NULL) float32
+ *  dstate    1 .. 64.
+ *  delta A <= 0 is expected, as for the other scans (a state that grows is computed
+ *  as long as its growth over 512 tokens fits a float32).
+ */
+typedef struct {
+    const void *x, *dt, *z, *B, *C;
+    const float *A, *D, *dt_bias;
+    long long x_stride, dt_stride, z_stride, b_stride, c_stride;
+    ssd_dtype io_dtype;
+    int softplus, channels, ngroups, dstate;
+} ssd_sel_args;
+
+/*
+ * The scan on packed sequences, one launch, no workspace.
+ *  state  [nslots, channels, dstate] float32, or NULL: every sequence from zero
+ *  chunk_states  NULL, or [ssd_selective_scan_chunk_states(tokens, nseq), channels,
+ *         dstate] float32: the states before every 128th token of each sequence,
+ *         which ssd_selective_scan_bwd reads (entries of no sequence stay unwritten)
+ *  y      [tokens, channels] io_dtype, contiguous
+ */
+size_t ssd_selective_scan_chunk_states(int tokens, int nseq);
+ssd_status ssd_selective_scan_varlen(const ssd_sel_args *args, const int *cu_seqlens, float *state,
+                                     const int *slots, const unsigned char *has_init,
+                                     float *chunk_states, void *y, int tokens, int nseq, int nslots,
+                                     void *stream);
+
+/* One token per sequence, state [nslots, channels, dstate] float32 in place,
+ * y [batch, channels].  batch <= 65535. */
+ssd_status ssd_selective_state_update(const ssd_sel_args *args, float *state, const int *slots,
+                                      void *y, int batch, int nslots, void *stream);
+
+/*
+ * Gradient of ssd_selective_scan_varlen without states: from dy [tokens, channels]
+ * io_dtype (contiguous) and the forward's chunk_states to dx, ddt, dz (NULL when z
+ * is) [tokens, channels] and dB, dC [tokens, ngroups, dstate] in io_dtype,
+ * contiguous, and dA [channels, dstate], dD and ddt_bias [channels] (or NULL)
+ * float32.  Sums run in a fixed order.  The states inside a chunk are formed
+ * again.  Two launches and a workspace.
+ */
+size_t ssd_selective_scan_bwd_workspace_size(int tokens, int nseq, int channels, int ngroups, int dstate);
+ssd_status ssd_selective_scan_bwd(const ssd_sel_args *args, const int *cu_seqlens, const void *dy,
+                                  const float *chunk_states, void *dx, void *ddt, void *dz, void *dB,
+                                  void *dC, float *dA, float *dD, float *ddt_bias, int tokens, int nseq,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The norm before a block, with the residual stream's update:
+ *
+ *   r = residual + scale * x,   out = r / sqrt(mean(r^2) + eps) * weight
+ *
+ *  x, out [rows, width] io_dtype;  residual, residual_out [rows, width]
+ *  residual_dtype (io_dtype or SSD_F32; residual NULL: zero; residual_out NULL: r
+ *  is not stored, else it may be residual itself when that is contiguous);
+ *  scale [width] float32 or NULL for 1;  weight [width] float32.
+ *  width 1 .. 8192.
+ */
+ssd_status ssd_residual_rmsnorm(const void *x, long long x_stride, const void *residual,
+                                long long residual_stride, const float *scale, const float *weight,
+                                void *out, void *residual_out, ssd_dtype io_dtype,
+                                ssd_dtype residual_dtype, int rows, int width, float eps,
+                                void *stream);
+
+/*
+ * Its gradient.  residual is the stored residual_out (the norm is taken again from
+ * it), dout the gradient at out, dresidual the one at residual_out (residual_dtype,
+ * or NULL for none).  Outputs: dresidual_in (residual_dtype) and dx (io_dtype),
+ * either may be NULL; dweight; and with scale given, which needs x, dscale.
+ * dresidual_in may be dresidual itself.  Two launches.
+ */
+size_t ssd_rmsnorm_bwd_workspace_size(int rows, int width);
+ssd_status ssd_residual_rmsnorm_bwd(const void *residual, long long residual_stride,
+                                    const float *weight, const void *dout, const void *dresidual,
+                                    const void *x, long long x_stride, const float *scale, void *dx,
+                                    void *dresidual_in, float *dweight, float *dscale,
+                                    ssd_dtype io_dtype, ssd_dtype residual_dtype, int rows, int width,
+                                    float eps, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The norm after a block's scan, with its gate, and (for a norm that closes a
+ * block) the residual and its scale:
+ *
+ *   n = v / sqrt(mean_group(v^2) + eps) * weight  with v = y silu(z), or
+ *   n = y / sqrt(mean_group(y^2) + eps) * weight * silu(z)   (norm_before_gate != 0)
+ *   out = n * scale + residual          (scale NULL: 1, residual NULL: 0)
+ *
+ *  y, z (NULL: no gate), residual, out [rows, width] io_dtype; means over the
+ *  width / ngroups channels of each group, at most 8192.  out may be residual.
+ */
+ssd_status ssd_gated_rmsnorm(const void *y, long long y_stride, const void *z, long long z_stride,
+                             const void *residual, long long residual_stride, const float *scale,
+                             const float *weight, void *out, ssd_dtype io_dtype, int rows, int width,
+                             int ngroups, int norm_before_gate, float eps, void *stream);
+
+/* Its gradient: dy, dz (NULL when z is), dweight, and dscale when scale is given;
+ * the residual's gradient is dout itself.  Workspace from
+ * ssd_rmsnorm_bwd_workspace_size(rows, width).  Two launches. */
+ssd_status ssd_gated_rmsnorm_bwd(const void *y, long long y_stride, const void *z, long long z_stride,
+                                 const float *weight, const void *dout, const float *scale, void *dy,
+                                 void *dz, float *dweight, float *dscale, ssd_dtype io_dtype, int rows,
+                                 int width, int ngroups, int norm_before_gate, float eps,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Waits for `stream`, then reports and clears an error that a kernel raised on
  * the device since the last call on this device (SSD_ERR_TIMEOUT when one of the
  * tensor-core kernel's bounded waits between its warp roles gave up after 1 s;
  * the kernel then stops at once and the outputs of that call are invalid), or a
- * CUDA error from the stream.
+ * CUDA error from the stream; SSD_ERR_INVALID_ARG when sequence bounds or slots
+ * in device memory were out of range (see the packed sequences above).
  * SSD_OK when there was none.
  */
 ssd_status ssd_get_device_status(void *stream);

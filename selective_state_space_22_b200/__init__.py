@@ -24,7 +24,10 @@ __all__ = ["SSDError", "ssd_scan_fwd", "ssd_scan_fwd_complex", "ssd_state_update
            "ssd_scan_fwd_noalloc", "ssd_last_error", "ssd_version", "load_library", "LIB_PATH",
            "SSD_WORKSPACE_INVALID", "ssd_scan_bwd", "ssd_scan_bwd_workspace_size",
            "ssd_scan_bwd_complex", "ssd_scan_bwd_complex_workspace_size", "ssd_scan_final_state",
-           "ssd_fold_states", "ssd_scan_fwd_complex_packed", "ssd_conv1d_xbc", "ssd_selective_scan"]
+           "ssd_fold_states", "ssd_scan_fwd_complex_packed", "ssd_conv1d_xbc", "ssd_selective_scan",
+           "ssd_conv1d_varlen", "ssd_conv1d_update", "ssd_conv1d_bwd", "ssd_selective_scan_varlen",
+           "ssd_selective_state_update", "ssd_selective_scan_bwd", "ssd_residual_rmsnorm",
+           "ssd_residual_rmsnorm_bwd", "ssd_gated_rmsnorm", "ssd_gated_rmsnorm_bwd"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libssd.so")
 
@@ -88,6 +91,7 @@ def load_library(path: str | None = None):
         lib.ssd_scan_final_state.restype = _I
         lib.ssd_fold_states.argtypes = [_VP, _VP, _I, _VP, _I, _I, _I, _I, _VP]
         lib.ssd_fold_states.restype = _I
+        declare_mixer(lib)
         lib.ssd_debug_inject_stall.argtypes = [_I, ctypes.c_ulonglong]
         lib.ssd_debug_inject_stall.restype = _I
         lib.ssd_get_device_status.argtypes = [_VP]
@@ -578,3 +582,8 @@ def ssd_scan_bwd_complex(x, dt, A, B, C, D, init_state, dy, dfinal=None, *, out=
 def ssd_get_device_status(stream=None) -> None:
     """Wait for the stream and raise SSDError if a kernel flagged a device-side error."""
     _check(load_library().ssd_get_device_status(_stream_handle(stream)))
+
+
+from .mixer import (declare_mixer, ssd_conv1d_bwd, ssd_conv1d_update, ssd_conv1d_varlen,  # noqa: E402
+                    ssd_gated_rmsnorm, ssd_gated_rmsnorm_bwd, ssd_residual_rmsnorm, ssd_residual_rmsnorm_bwd,
+                    ssd_selective_scan_bwd, ssd_selective_scan_varlen, ssd_selective_state_update)

@@ -1,0 +1,440 @@
+// norms.cu -- the norms before and after a mixer block, with the residual, its
+// scale and the gate in the same pass, and their gradients.
+//
+//   before:  r = res + scale x,  out = r rstd(r) w,        rstd(v) = 1/sqrt(mean v^2 + eps)
+//   after:   gate first: n = v rstd(v) w with v = y silu(z);  norm first: n = y rstd(y) w silu(z);
+//            out = n, or res + scale n;  rstd per group of width/groups channels.
+//
+// Gradients with m = v rstd and dn the gradient at m:
+//   dv = rstd (dn - m mean(dn m)),  dw = sum_rows d(out) m,  dscale = sum_rows dout (what it scales).
+//
+// Bound by HBM: every row is read once and written once.  A unit (one row, or one
+// group of a row) is held in the registers of TPR threads, V neighbouring channels
+// (16 bytes of the io type) a vector and VPT vectors a thread; its sums go through
+// shuffles and, past one warp, shared memory.  The gradients need both of their
+// sums (v^2 and dn v) only after all loads, so one round of sums serves them.
+// There a thread keeps its columns over all rows its block takes and sums dw and
+// dscale in registers; norm_bwd_sum adds the blocks' parts in a fixed order.
+#include <type_traits>
+
+#include "mixer.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int BWD_BLOCKS = 592;  // 4 blocks of 256 threads per SM on 148 SMs
+
+// Sums of (a, b) over the TPR threads of a unit; every thread of the block calls it.
+template <int TPR> __device__ __forceinline__ float2 unit_sum(float2 v, float2 *sh) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+    if constexpr (TPR > 32) {
+        constexpr int W = TPR / 32;
+        const int wid = threadIdx.x >> 5;
+        __syncthreads();  // sh free again
+        if ((threadIdx.x & 31) == 0) sh[wid] = v;
+        __syncthreads();
+        v = sh[wid / W * W];
+#pragma unroll
+        for (int i = 1; i < W; ++i) {
+            const float2 u = sh[wid / W * W + i];
+            v.x += u.x, v.y += u.y;
+        }
+    }
+    return v;
+}
+
+template <int TPR> constexpr int block_threads() { return TPR < 128 ? 128 : TPR; }
+
+template <typename T, typename TR, int V, int VPT, int TPR>
+__global__ void __launch_bounds__(block_threads<TPR>()) norm_before_kernel(NormCall c) {
+    constexpr bool WIDE = V > 1;
+    __shared__ float2 sh[block_threads<TPR>() / 32];
+    const int t = threadIdx.x % TPR, row = blockIdx.x * (block_threads<TPR>() / TPR) + threadIdx.x / TPR;
+    const bool in = row < c.rows;
+    const T *x = static_cast<const T *>(c.x) + row * c.ld_x;
+    const TR *res = static_cast<const TR *>(c.res) + row * c.ld_res;
+    float r[VPT][V];
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < VPT; ++q) {
+        const int k = (q * TPR + t) * V;
+#pragma unroll
+        for (int v = 0; v < V; ++v) r[q][v] = 0.f;
+        if (!in || k >= c.width) continue;
+        load_v<T, V, WIDE>(x + k, r[q]);
+        if (c.scale) {
+            float a[V];
+            load_v<float, V, WIDE>(c.scale + k, a);
+#pragma unroll
+            for (int v = 0; v < V; ++v) r[q][v] *= a[v];
+        }
+        if (c.res) {
+            float a[V];
+            load_v<TR, V, WIDE>(res + k, a);
+#pragma unroll
+            for (int v = 0; v < V; ++v) r[q][v] += a[v];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) s.x = fmaf(r[q][v], r[q][v], s.x);
+    }
+    s = unit_sum<TPR>(s, sh);
+    if (!in) return;
+    const float rstd = 1.f / sqrtf(s.x / c.width + c.eps);
+#pragma unroll
+    for (int q = 0; q < VPT; ++q) {
+        const int k = (q * TPR + t) * V;
+        if (k >= c.width) continue;
+        if (c.res_out) store_v<TR, V, WIDE>(static_cast<TR *>(c.res_out) + (size_t)row * c.width + k, r[q]);
+        float w[V];
+        load_v<float, V, WIDE>(c.w + k, w);
+#pragma unroll
+        for (int v = 0; v < V; ++v) r[q][v] *= rstd * w[v];
+        store_v<T, V, WIDE>(static_cast<T *>(c.out) + (size_t)row * c.width + k, r[q]);
+    }
+}
+
+// blockIdx.y: the group.
+template <typename T, int V, int VPT, int TPR>
+__global__ void __launch_bounds__(block_threads<TPR>()) norm_after_kernel(NormCall c) {
+    constexpr bool WIDE = V > 1;
+    __shared__ float2 sh[block_threads<TPR>() / 32];
+    const int t = threadIdx.x % TPR, row = blockIdx.x * (block_threads<TPR>() / TPR) + threadIdx.x / TPR;
+    const int gw = c.width / c.groups, g0 = blockIdx.y * gw;
+    const bool in = row < c.rows;
+    const T *y = static_cast<const T *>(c.x) + row * c.ld_x + g0, *z = static_cast<const T *>(c.z) + row * c.ld_z + g0;
+    float a[VPT][V], gate[VPT][V];
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < VPT; ++q) {
+        const int k = (q * TPR + t) * V;
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[q][v] = 0.f, gate[q][v] = 1.f;
+        if (!in || k >= gw) continue;
+        load_v<T, V, WIDE>(y + k, a[q]);
+        if (c.z) {
+            load_v<T, V, WIDE>(z + k, gate[q]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                gate[q][v] = silu_v(gate[q][v]);
+                if (!c.norm_first) a[q][v] *= gate[q][v];
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) s.x = fmaf(a[q][v], a[q][v], s.x);
+    }
+    s = unit_sum<TPR>(s, sh);
+    if (!in) return;
+    const float rstd = 1.f / sqrtf(s.x / gw + c.eps);
+#pragma unroll
+    for (int q = 0; q < VPT; ++q) {
+        const int k = (q * TPR + t) * V;
+        if (k >= gw) continue;
+        float w[V];
+        load_v<float, V, WIDE>(c.w + g0 + k, w);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            a[q][v] *= rstd * w[v];
+            if (c.norm_first) a[q][v] *= gate[q][v];
+        }
+        if (c.scale) {
+            load_v<float, V, WIDE>(c.scale + g0 + k, w);
+#pragma unroll
+            for (int v = 0; v < V; ++v) a[q][v] *= w[v];
+        }
+        if (c.res) {
+            load_v<T, V, WIDE>(static_cast<const T *>(c.res) + row * c.ld_res + g0 + k, w);
+#pragma unroll
+            for (int v = 0; v < V; ++v) a[q][v] += w[v];
+        }
+        store_v<T, V, WIDE>(static_cast<T *>(c.out) + (size_t)row * c.width + g0 + k, a[q]);
+    }
+}
+
+// A block's sums over its rows, added over its units, into part[blockIdx.x][width]
+// (and the dscale half after all blocks' dw).
+template <int V, int VPT, int TPR>
+__device__ __forceinline__ void put_parts(const float (&dw)[VPT][V], const float (&ds)[VPT][V], bool scaled, int g0, int gw,
+                                          int width, float *part, float *sh) {
+    constexpr int U = block_threads<TPR>() / TPR;
+    const int t = threadIdx.x % TPR, unit = threadIdx.x / TPR;
+    for (int what = 0; what < (scaled ? 2 : 1); ++what) {
+        float *o = part + ((size_t)what * gridDim.x + blockIdx.x) * width + g0;
+#pragma unroll
+        for (int q = 0; q < VPT; ++q)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int k = (q * TPR + t) * V + v;
+                float s = what ? ds[q][v] : dw[q][v];
+                if constexpr (U > 1) {
+                    __syncthreads();
+                    sh[threadIdx.x] = s;
+                    __syncthreads();
+                    if (unit == 0)
+#pragma unroll
+                        for (int i = 1; i < U; ++i) s += sh[i * TPR + t];
+                }
+                if (unit == 0 && k < gw) o[k] = s;
+            }
+    }
+}
+
+template <typename T, typename TR, int V, int VPT, int TPR>
+__global__ void __launch_bounds__(block_threads<TPR>()) norm_before_bwd_kernel(NormCall c, float *part) {
+    constexpr bool WIDE = V > 1;
+    constexpr int U = block_threads<TPR>() / TPR;
+    __shared__ float2 sh[block_threads<TPR>() / 32];
+    __shared__ float sums[U > 1 ? block_threads<TPR>() : 1];
+    const int t = threadIdx.x % TPR, unit = threadIdx.x / TPR;
+    float dw[VPT][V], ds[VPT][V], w[VPT][V];
+#pragma unroll
+    for (int q = 0; q < VPT; ++q) {
+        const int k = (q * TPR + t) * V;
+#pragma unroll
+        for (int v = 0; v < V; ++v) dw[q][v] = ds[q][v] = w[q][v] = 0.f;
+        if (k < c.width) load_v<float, V, WIDE>(c.w + k, w[q]);
+    }
+    for (int row0 = blockIdx.x * U; row0 < c.rows; row0 += gridDim.x * U) {
+        const int row = row0 + unit;
+        const bool in = row < c.rows;
+        float r[VPT][V], d[VPT][V];
+        float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < VPT; ++q) {
+            const int k = (q * TPR + t) * V;
+#pragma unroll
+            for (int v = 0; v < V; ++v) r[q][v] = d[q][v] = 0.f;
+            if (!in || k >= c.width) continue;
+            load_v<TR, V, WIDE>(static_cast<const TR *>(c.res) + row * c.ld_res + k, r[q]);
+            load_v<T, V, WIDE>(static_cast<const T *>(c.dout) + (size_t)row * c.width + k, d[q]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                s.x = fmaf(r[q][v], r[q][v], s.x);
+                s.y = fmaf(d[q][v] * w[q][v], r[q][v], s.y);
+            }
+        }
+        s = unit_sum<TPR>(s, sh);
+        const float rstd = 1.f / sqrtf(s.x / c.width + c.eps), m = s.y * rstd / c.width;
+#pragma unroll
+        for (int q = 0; q < VPT; ++q) {
+            const int k = (q * TPR + t) * V;
+            if (!in || k >= c.width) continue;
+            float a[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float n = r[q][v] * rstd;
+                dw[q][v] = fmaf(d[q][v], n, dw[q][v]);
+                d[q][v] = rstd * (d[q][v] * w[q][v] - n * m);
+            }
+            if (c.dres) {
+                load_v<TR, V, WIDE>(static_cast<const TR *>(c.dres) + (size_t)row * c.width + k, a);
+#pragma unroll
+                for (int v = 0; v < V; ++v) d[q][v] += a[v];
+            }
+            if (c.dres_out) store_v<TR, V, WIDE>(static_cast<TR *>(c.dres_out) + (size_t)row * c.width + k, d[q]);
+            if (c.scale) {
+                load_v<T, V, WIDE>(static_cast<const T *>(c.x) + row * c.ld_x + k, a);
+#pragma unroll
+                for (int v = 0; v < V; ++v) ds[q][v] = fmaf(d[q][v], a[v], ds[q][v]);
+                load_v<float, V, WIDE>(c.scale + k, a);
+#pragma unroll
+                for (int v = 0; v < V; ++v) d[q][v] *= a[v];
+            }
+            if (c.dx) store_v<T, V, WIDE>(static_cast<T *>(c.dx) + (size_t)row * c.width + k, d[q]);
+        }
+    }
+    put_parts<V, VPT, TPR>(dw, ds, c.scale != nullptr, 0, c.width, c.width, part, sums);
+}
+
+template <typename T, int V, int VPT, int TPR>
+__global__ void __launch_bounds__(block_threads<TPR>()) norm_after_bwd_kernel(NormCall c, float *part) {
+    constexpr bool WIDE = V > 1;
+    constexpr int U = block_threads<TPR>() / TPR;
+    __shared__ float2 sh[block_threads<TPR>() / 32];
+    __shared__ float sums[U > 1 ? block_threads<TPR>() : 1];
+    const int t = threadIdx.x % TPR, unit = threadIdx.x / TPR;
+    const int gw = c.width / c.groups, g0 = blockIdx.y * gw;
+    float dw[VPT][V], ds[VPT][V], w[VPT][V];
+#pragma unroll
+    for (int q = 0; q < VPT; ++q) {
+        const int k = (q * TPR + t) * V;
+#pragma unroll
+        for (int v = 0; v < V; ++v) dw[q][v] = ds[q][v] = w[q][v] = 0.f;
+        if (k < gw) load_v<float, V, WIDE>(c.w + g0 + k, w[q]);
+    }
+    for (int row0 = blockIdx.x * U; row0 < c.rows; row0 += gridDim.x * U) {
+        const int row = row0 + unit;
+        const bool in = row < c.rows;
+        float y[VPT][V], z[VPT][V], d[VPT][V];
+        float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < VPT; ++q) {
+            const int k = (q * TPR + t) * V;
+#pragma unroll
+            for (int v = 0; v < V; ++v) y[q][v] = z[q][v] = d[q][v] = 0.f;
+            if (!in || k >= gw) continue;
+            load_v<T, V, WIDE>(static_cast<const T *>(c.x) + row * c.ld_x + g0 + k, y[q]);
+            if (c.z) load_v<T, V, WIDE>(static_cast<const T *>(c.z) + row * c.ld_z + g0 + k, z[q]);
+            load_v<T, V, WIDE>(static_cast<const T *>(c.dout) + (size_t)row * c.width + g0 + k, d[q]);
+            float a[V];
+            if (c.scale) load_v<float, V, WIDE>(c.scale + g0 + k, a);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float gate = c.z ? silu_v(z[q][v]) : 1.f;
+                const float vv = c.norm_first ? y[q][v] : y[q][v] * gate;
+                const float dn = d[q][v] * (c.scale ? a[v] : 1.f) * (c.norm_first ? gate : 1.f) * w[q][v];
+                s.x = fmaf(vv, vv, s.x);
+                s.y = fmaf(dn, vv, s.y);
+            }
+        }
+        s = unit_sum<TPR>(s, sh);
+        const float rstd = 1.f / sqrtf(s.x / gw + c.eps), m = s.y * rstd / gw;
+#pragma unroll
+        for (int q = 0; q < VPT; ++q) {
+            const int k = (q * TPR + t) * V;
+            if (!in || k >= gw) continue;
+            float a[V], dy[V], dz[V];
+            if (c.scale) load_v<float, V, WIDE>(c.scale + g0 + k, a);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float sg = c.z ? sigmoid_f(z[q][v]) : 1.f, gate = c.z ? z[q][v] * sg : 1.f;
+                const float dgate = sg * fmaf(z[q][v], 1.f - sg, 1.f);  // silu'(z)
+                const float n = (c.norm_first ? y[q][v] : y[q][v] * gate) * rstd;
+                const float normed = n * w[q][v];
+                if (c.scale) ds[q][v] = fmaf(d[q][v], c.norm_first ? normed * gate : normed, ds[q][v]);
+                const float dg = c.scale ? d[q][v] * a[v] : d[q][v];  // at the norm's (gated) result
+                const float dm = c.norm_first ? dg * gate : dg;
+                dw[q][v] = fmaf(dm, n, dw[q][v]);
+                const float dv = rstd * (dm * w[q][v] - n * m);
+                dy[v] = c.norm_first ? dv : dv * gate;
+                dz[v] = (c.norm_first ? dg * normed : dv * y[q][v]) * dgate;
+            }
+            const size_t o = (size_t)row * c.width + g0 + k;
+            store_v<T, V, WIDE>(static_cast<T *>(c.dx) + o, dy);
+            if (c.z) store_v<T, V, WIDE>(static_cast<T *>(c.dz) + o, dz);
+        }
+    }
+    put_parts<V, VPT, TPR>(dw, ds, c.scale != nullptr, g0, gw, c.width, part, sums);
+}
+
+// dw (blockIdx.y 0) or dscale (1) from the blocks' parts.
+__global__ void __launch_bounds__(256) norm_bwd_sum(const float *__restrict__ part, int parts, int width,
+                                                   float *__restrict__ dw, float *__restrict__ ds) {
+    __shared__ float s[8][33];
+    const int k = blockIdx.x * 32 + (threadIdx.x & 31), q = threadIdx.x >> 5;
+    const float *p = part + (size_t)blockIdx.y * parts * width;
+    float a = 0.f;
+    if (k < width)
+        for (int i = q; i < parts; i += 8) a += p[(size_t)i * width + k];
+    s[q][threadIdx.x & 31] = a;
+    __syncthreads();
+    if (q || k >= width) return;
+    for (int i = 1; i < 8; ++i) a += s[i][threadIdx.x];
+    (blockIdx.y ? ds : dw)[k] = a;
+}
+
+// Calls f with the unit's split: TPR threads (a power of two, MIN .. 512) of VPT
+// vectors of V channels.  One vector per thread up to 512 threads; four (then 16)
+// single channels where rows are not aligned vectors.
+template <int VPT, int MIN, typename F> cudaError_t with_tpr(int vectors, F &&f) {
+    const int need = (vectors + VPT - 1) / VPT;
+    constexpr std::integral_constant<int, VPT> vpt{};
+    if constexpr (MIN <= 32)
+        if (need <= 32) return f(vpt, std::integral_constant<int, 32>{});
+    if constexpr (MIN <= 64)
+        if (need <= 64) return f(vpt, std::integral_constant<int, 64>{});
+    if constexpr (MIN <= 128)
+        if (need <= 128) return f(vpt, std::integral_constant<int, 128>{});
+    if constexpr (MIN <= 256)
+        if (need <= 256) return f(vpt, std::integral_constant<int, 256>{});
+    return f(vpt, std::integral_constant<int, 512>{});
+}
+template <int V, typename F> cudaError_t with_split(int width, F &&f) {
+    static_assert(NORM_MAX_WIDTH == 8192, "the splits below end there");
+    const int vectors = (width + V - 1) / V;
+    if constexpr (V == 1) {
+        return vectors <= 2048 ? with_tpr<4, 32>(vectors, f) : with_tpr<16, 256>(vectors, f);
+    } else {
+        if (vectors <= 512) return with_tpr<1, 32>(vectors, f);
+        if constexpr (V == 4)
+            if (vectors > 1024) return with_tpr<4, 512>(vectors, f);
+        return with_tpr<2, 512>(vectors, f);
+    }
+}
+
+template <typename T, typename TR, int V> cudaError_t run_before(const NormCall &c, cudaStream_t st) {
+    return with_split<V>(c.width, [&](auto vpt, auto tpr) {
+        constexpr int TH = block_threads<tpr()>(), U = TH / tpr();
+        norm_before_kernel<T, TR, V, vpt(), tpr()><<<(c.rows + U - 1) / U, TH, 0, st>>>(c);
+        return cudaGetLastError();
+    });
+}
+template <typename T, int V> cudaError_t run_after(const NormCall &c, cudaStream_t st) {
+    return with_split<V>(c.width / c.groups, [&](auto vpt, auto tpr) {
+        constexpr int TH = block_threads<tpr()>(), U = TH / tpr();
+        norm_after_kernel<T, V, vpt(), tpr()><<<dim3((c.rows + U - 1) / U, c.groups), TH, 0, st>>>(c);
+        return cudaGetLastError();
+    });
+}
+int bwd_blocks(int rows, int units) { return min((rows + units - 1) / units, BWD_BLOCKS); }
+cudaError_t run_sum(const NormCall &c, const float *ws, int parts, cudaStream_t st) {
+    norm_bwd_sum<<<dim3((c.width + 31) / 32, c.scale ? 2 : 1), 256, 0, st>>>(ws, parts, c.width, c.dw, c.dscale);
+    return cudaGetLastError();
+}
+template <typename T, typename TR, int V> cudaError_t run_before_bwd(const NormCall &c, float *ws, cudaStream_t st) {
+    return with_split<V>(c.width, [&](auto vpt, auto tpr) {
+        constexpr int TH = block_threads<tpr()>(), U = TH / tpr();
+        const int blocks = bwd_blocks(c.rows, U);
+        if (blocks > 0) norm_before_bwd_kernel<T, TR, V, vpt(), tpr()><<<blocks, TH, 0, st>>>(c, ws);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? run_sum(c, ws, blocks, st) : e;
+    });
+}
+template <typename T, int V> cudaError_t run_after_bwd(const NormCall &c, float *ws, cudaStream_t st) {
+    return with_split<V>(c.width / c.groups, [&](auto vpt, auto tpr) {
+        constexpr int TH = block_threads<tpr()>(), U = TH / tpr();
+        const int blocks = bwd_blocks(c.rows, U);
+        if (blocks > 0) norm_after_bwd_kernel<T, V, vpt(), tpr()><<<dim3(blocks, c.groups), TH, 0, st>>>(c, ws);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? run_sum(c, ws, blocks, st) : e;
+    });
+}
+
+// Whether every row (and group) can be read as vectors of V channels; `V` floats
+// are read as 16-byte accesses, so 16-byte alignment serves every type.
+bool wide_rows(const NormCall &c, int V) {
+    const size_t e = c.bf16 ? 2 : 4, er = c.res_bf16 ? 2 : 4;
+    return c.width % V == 0 && (c.width / c.groups) % V == 0 && (!c.x || rows_aligned(c.x, c.ld_x, e, 16)) &&
+           (!c.z || rows_aligned(c.z, c.ld_z, e, 16)) && (!c.res || rows_aligned(c.res, c.ld_res, er, 16));
+}
+
+}  // namespace
+
+cudaError_t launch_norm_before(const NormCall &c, cudaStream_t st) {
+    using H = __nv_bfloat16;
+    if (!c.bf16) return wide_rows(c, 4) ? run_before<float, float, 4>(c, st) : run_before<float, float, 1>(c, st);
+    if (c.res_bf16) return wide_rows(c, 8) ? run_before<H, H, 8>(c, st) : run_before<H, H, 1>(c, st);
+    return wide_rows(c, 8) ? run_before<H, float, 8>(c, st) : run_before<H, float, 1>(c, st);
+}
+cudaError_t launch_norm_after(const NormCall &c, cudaStream_t st) {
+    using H = __nv_bfloat16;
+    if (!c.bf16) return wide_rows(c, 4) ? run_after<float, 4>(c, st) : run_after<float, 1>(c, st);
+    return wide_rows(c, 8) ? run_after<H, 8>(c, st) : run_after<H, 1>(c, st);
+}
+size_t norm_bwd_workspace(int rows, int width) { return 2 * (size_t)min(rows, BWD_BLOCKS) * width * sizeof(float); }
+cudaError_t launch_norm_before_bwd(const NormCall &c, float *ws, cudaStream_t st) {
+    using H = __nv_bfloat16;
+    if (!c.bf16) return wide_rows(c, 4) ? run_before_bwd<float, float, 4>(c, ws, st) : run_before_bwd<float, float, 1>(c, ws, st);
+    if (c.res_bf16) return wide_rows(c, 8) ? run_before_bwd<H, H, 8>(c, ws, st) : run_before_bwd<H, H, 1>(c, ws, st);
+    return wide_rows(c, 8) ? run_before_bwd<H, float, 8>(c, ws, st) : run_before_bwd<H, float, 1>(c, ws, st);
+}
+cudaError_t launch_norm_after_bwd(const NormCall &c, float *ws, cudaStream_t st) {
+    using H = __nv_bfloat16;
+    if (!c.bf16) return wide_rows(c, 4) ? run_after_bwd<float, 4>(c, ws, st) : run_after_bwd<float, 1>(c, ws, st);
+    return wide_rows(c, 8) ? run_after_bwd<H, 8>(c, ws, st) : run_after_bwd<H, 1>(c, ws, st);
+}
+
+}  // namespace ssd

@@ -1,0 +1,380 @@
+// selscan_bwd.cu -- the gradient of the gated Mamba-1 scan on packed sequences.
+//
+// With a_t = exp(delta_t A), y = p silu(z), p = sum_n C h + D x and dp = dy silu(z):
+//   g_t = dp_t C_t + a_{t+1} g_{t+1}            (the gradient at h_t, per state)
+//   dC_t = sum_d dp_t h_t,  dB_t = sum_d delta_t x_t g_t          (over a group's channels)
+//   du_t = sum_n g_t B_t,   q_t = g_t a_t h_{t-1},  dA = sum_t delta_t q_t
+//   ddelta_t = x_t du_t + sum_n A q_t,  dx_t = delta_t du_t + D dp_t,  dD = sum_t dp_t x_t
+//   dz_t = dy_t p_t silu'(z_t),  ddt_t = ddelta_t softplus'(dt_t + bias),  dbias = sum_t ddt_t.
+//
+// A block takes one sequence and CB channels and walks the chunks backwards.  In a
+// chunk each state is run forwards from the kept chunk state (a and h_{t-1} stay in
+// registers, so the exponentials are taken once) and then backwards, both split
+// over the lanes of a channel as in the forward.  dB and dC are summed over a
+// warp's channels by shuffles that halve the values with each step, over the
+// block's warps in shared memory (each step of the state loop gives every warp
+// another state, so there are no atomics and one fixed order), and over blocks by
+// sel_bwd_sum.  Bound by issue: some 20 operations per state and token.
+#include "selscan_tile.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int TL = 8, K = 16, SEG = TL * K, CL = 32 / TL, CB = SEL_WARPS * CL;
+static_assert(SEG == SEL_CHUNK, "a chunk starts where its state was kept");
+
+template <typename T> struct BwdShape {
+    using Rows = RowTile<T, SEG, CB, TL>;
+    using BC = BCTile<T, SEG, TL>;
+    static size_t smem(int N) {
+        return 4 * (size_t)Rows::BYTES + (size_t)N * BC::STATE_WORDS * 4 + 2 * (size_t)N * SEG * 4 + 4 * (size_t)CB * N * 4;
+    }
+};
+
+struct Parts {      // workspace
+    float *bc;      // [groups * tiles][tokens][2][dstate]
+    float *a;       // [nseq][channels][dstate]
+    float *d;       // [nseq][2][channels]: dD, dbias
+};
+
+template <typename T>
+__global__ void __launch_bounds__(SEL_WARPS * 32, 1) sel_bwd_kernel(SelCall c, Parts parts, bool wide, bool wide_bc) {
+    using S = BwdShape<T>;
+    using Rows = typename S::Rows;
+    using BC = typename S::BC;
+    extern __shared__ __align__(16) unsigned char smem[];
+    unsigned char *xs = smem, *ds = xs + Rows::BYTES, *zs = ds + Rows::BYTES, *ys = zs + Rows::BYTES;
+    uint32_t *bc = reinterpret_cast<uint32_t *>(ys + Rows::BYTES);
+    const int N = c.dstate;
+    float *sB = reinterpret_cast<float *>(bc + N * BC::STATE_WORDS), *sC = sB + N * SEG;  // sums over the block's channels
+    float *As = sC + N * SEG, *hs = As + CB * N, *gs = hs + CB * N, *dAs = gs + CB * N;   // [n][channel]
+
+    const int i = blockIdx.x;
+    const int per_group = c.channels / c.groups, tiles = (per_group + CB - 1) / CB;
+    const int g = blockIdx.y / tiles, c0 = g * per_group + (blockIdx.y % tiles) * CB;
+    const int cols = min(CB, (g + 1) * per_group - c0);
+    int lo, hi;
+    if (!seq_rows(c.seq, i, lo, hi)) lo = hi = 0;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, l = lane % TL, cl = lane / TL, ch = w * CL + cl;
+    const int chc = min(ch, cols - 1);
+    const float bias = c.dt_bias ? c.dt_bias[c0 + chc] : 0.f, Dv = c.D ? c.D[c0 + chc] : 0.f;
+    const T *x = static_cast<const T *>(c.x) + c0, *dt = static_cast<const T *>(c.dt) + c0,
+            *z = static_cast<const T *>(c.z) + c0, *dy = static_cast<const T *>(c.dy) + c0;
+    const T *B = static_cast<const T *>(c.B) + g * N, *C = static_cast<const T *>(c.C) + g * N;
+    for (int u = threadIdx.x; u < CB * N; u += SEL_WARPS * 32) {
+        const int cc = u / N, n = u - cc * N;
+        As[n * CB + cc] = cc < cols ? c.A[(size_t)c0 * N + u] * LOG2E : 0.f;
+        gs[n * CB + cc] = dAs[n * CB + cc] = 0.f;
+    }
+    float dD = 0.f, dbias = 0.f;
+    const int chunks = (hi - lo + SEG - 1) / SEG, M = max(N, SEL_WARPS);
+    for (int chunk = chunks - 1; chunk >= 0; --chunk) {
+        const int t0 = lo + chunk * SEG, n = min(SEG, hi - t0), len = ((n + TL - 1) / TL + 3) & ~3;
+        __syncthreads();  // the tiles are free again
+        Rows::fetch(xs, x + t0 * c.ld_x, c.ld_x, n, cols, len, wide);
+        Rows::fetch(ds, dt + t0 * c.ld_dt, c.ld_dt, n, cols, len, wide);
+        if (c.z) Rows::fetch(zs, z + t0 * c.ld_z, c.ld_z, n, cols, len, wide);
+        Rows::fetch(ys, dy + (size_t)t0 * c.channels, c.channels, n, cols, len, wide);
+        cp_commit();
+        BC::fetch(bc, B + t0 * c.ld_b, c.ld_b, C + t0 * c.ld_c, c.ld_c, n, N, len, wide_bc);
+        const float *kept = c.chunk_states + ((size_t)(lo / SEL_CHUNK + i + chunk) * c.channels + c0) * N;
+        for (int u = threadIdx.x; u < CB * N; u += SEL_WARPS * 32)
+            hs[(u % N) * CB + u / N] = u < cols * N ? kept[u] : 0.f;
+        for (int u = threadIdx.x; u < N * SEG; u += SEL_WARPS * 32) sB[u] = sC[u] = 0.f;
+        cp_wait<0>();
+        __syncthreads();
+        const int mine = ch < cols ? max(0, min(len, n - l * len)) : 0;
+        float2 dl[K / 2], u2[K / 2], dp[K / 2], du[K / 2], sd[K / 2], p2[K / 2];
+        float total = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float d = 0.f, u = 0.f, e = 0.f;
+            if (k < mine) {
+                const int r = l * len + k;
+                d = ld_f32<T>(Rows::row(ds, r, l) + ch) + bias;
+                if (c.softplus) d = softplus_f(d);
+                u = d * ld_f32<T>(Rows::row(xs, r, l) + ch);
+                e = ld_f32<T>(Rows::row(ys, r, l) + ch);
+                if (c.z) e *= silu_v(ld_f32<T>(Rows::row(zs, r, l) + ch));
+            }
+            total += d;
+            if (k & 1)
+                dl[k / 2].y = d, u2[k / 2].y = u, dp[k / 2].y = e;
+            else
+                dl[k / 2].x = d, u2[k / 2].x = u, dp[k / 2].x = e;
+        }
+#pragma unroll
+        for (int k = 0; k < K / 2; ++k) du[k] = sd[k] = p2[k] = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int it = 0; it < M; ++it) {
+            const int s = it + w < M ? it + w : it + w - M;
+            if (s < N) {
+                const float A2 = As[s * CB + ch], hc = hs[s * CB + ch], gc = gs[s * CB + ch];
+                const float2 A22 = splat(A2);
+                float2 a2[K / 2], hp[K / 2], v2[K / 2];
+                // forwards: v2 holds the inputs, then dp h
+                float S_ = 0.f, P = ex2a(A2 * total);
+                const float P0 = P;
+#pragma unroll
+                for (int q = 0; q < K / 4; ++q) {
+                    if (4 * q >= len) break;
+                    float b[4], cv[4];
+                    BC::quad(bc, s, q, l, b, cv);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int k = 2 * q + j;
+                        const float2 arg = mul2(dl[k], A22);
+                        a2[k] = make_float2(ex2a(arg.x), ex2a(arg.y));
+                        v2[k] = mul2(u2[k], make_float2(b[2 * j], b[2 * j + 1]));
+                        S_ = fmaf(a2[k].x, S_, v2[k].x);
+                        S_ = fmaf(a2[k].y, S_, v2[k].y);
+                    }
+                }
+                if (l == 0) S_ = fmaf(P, hc, S_);
+#pragma unroll
+                for (int o = 1; o < TL; o *= 2) {
+                    const float Sp = __shfl_up_sync(0xffffffffu, S_, o, TL), Pp = __shfl_up_sync(0xffffffffu, P, o, TL);
+                    if (l >= o) S_ = fmaf(P, Sp, S_), P *= Pp;
+                }
+                float h = __shfl_up_sync(0xffffffffu, S_, 1, TL);
+                if (l == 0) h = hc;
+                float R = 0.f;
+#pragma unroll
+                for (int q = 0; q < K / 4; ++q) {
+                    if (4 * q >= len) break;
+                    float b[4], cv[4];
+                    BC::quad(bc, s, q, l, b, cv);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int k = 2 * q + j;
+                        float2 hh;
+                        hp[k].x = h;
+                        hh.x = h = fmaf(a2[k].x, h, v2[k].x);
+                        hp[k].y = h;
+                        hh.y = h = fmaf(a2[k].y, h, v2[k].y);
+                        p2[k] = fma2(make_float2(cv[2 * j], cv[2 * j + 1]), hh, p2[k]);
+                        v2[k] = mul2(dp[k], hh);
+                    }
+                }
+                // dC of the warp's channels: lane cl ends with tokens 4 cl .. 4 cl + 3
+                float sum[4];
+                auto reduce = [&] {
+                    float v8[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // cl bit 1: the run's halves
+                        const float2 keep = cl & 2 ? v2[k + 4] : v2[k], give = cl & 2 ? v2[k] : v2[k + 4];
+                        v8[2 * k] = keep.x + __shfl_xor_sync(0xffffffffu, give.x, 2 * TL);
+                        v8[2 * k + 1] = keep.y + __shfl_xor_sync(0xffffffffu, give.y, 2 * TL);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // cl bit 0: quads
+                        const float keep = cl & 1 ? v8[k + 4] : v8[k], give = cl & 1 ? v8[k] : v8[k + 4];
+                        sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, TL);
+                    }
+                };
+                auto add_to = [&](float *acc) {
+                    float4 *o = reinterpret_cast<float4 *>(acc + s * SEG + (cl * TL + l) * 4);
+                    float4 v = *o;
+                    v.x += sum[0], v.y += sum[1], v.z += sum[2], v.w += sum[3];
+                    *o = v;
+                };
+                if (len < K)
+#pragma unroll
+                    for (int k = 0; k < K / 2; ++k)
+                        if (2 * k >= len) v2[k] = make_float2(0.f, 0.f);
+                reduce();
+                if (4 * cl < len) add_to(sC);
+                // backwards: G = a g, what a token hands to the one before it
+                P = P0;
+#pragma unroll
+                for (int q = K / 4 - 1; q >= 0; --q) {
+                    if (4 * q >= len) continue;
+                    float b[4], cv[4];
+                    BC::quad(bc, s, q, l, b, cv);
+#pragma unroll
+                    for (int j = 1; j >= 0; --j) {
+                        const int k = 2 * q + j;
+                        v2[k] = mul2(dp[k], make_float2(cv[2 * j], cv[2 * j + 1]));
+                        R = a2[k].y * (R + v2[k].y);
+                        R = a2[k].x * (R + v2[k].x);
+                    }
+                }
+                if (l == TL - 1) R = fmaf(P, gc, R);
+#pragma unroll
+                for (int o = 1; o < TL; o *= 2) {
+                    const float Rn = __shfl_down_sync(0xffffffffu, R, o, TL), Pn = __shfl_down_sync(0xffffffffu, P, o, TL);
+                    if (l + o < TL) R = fmaf(P, Rn, R), P *= Pn;
+                }
+                float G = __shfl_down_sync(0xffffffffu, R, 1, TL);
+                if (l == TL - 1) G = gc;
+                if (l == 0) gs[s * CB + ch] = R;
+                float2 dA2 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int q = K / 4 - 1; q >= 0; --q) {
+                    if (4 * q >= len) continue;
+                    float b[4], cv[4];
+                    BC::quad(bc, s, q, l, b, cv);
+#pragma unroll
+                    for (int j = 1; j >= 0; --j) {
+                        const int k = 2 * q + j;
+                        float2 gg, GG;
+                        gg.y = G + v2[k].y, GG.y = G = a2[k].y * gg.y;
+                        gg.x = G + v2[k].x, GG.x = G = a2[k].x * gg.x;
+                        const float2 qq = mul2(GG, hp[k]);
+                        du[k] = fma2(gg, make_float2(b[2 * j], b[2 * j + 1]), du[k]);
+                        sd[k] = fma2(A22, qq, sd[k]);
+                        dA2 = fma2(dl[k], qq, dA2);
+                        v2[k] = mul2(u2[k], gg);
+                    }
+                }
+                if (len < K)
+#pragma unroll
+                    for (int k = 0; k < K / 2; ++k)
+                        if (2 * k >= len) v2[k] = make_float2(0.f, 0.f);
+                reduce();
+                if (4 * cl < len) add_to(sB);
+                float dA = dA2.x + dA2.y;
+#pragma unroll
+                for (int o = 1; o < TL; o *= 2) dA += __shfl_xor_sync(0xffffffffu, dA, o);
+                if (l == 0) dAs[s * CB + ch] += dA;
+            }
+            __syncthreads();  // the next state's sums
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (k < mine) {
+                const int r = l * len + k;
+                const float d = k & 1 ? dl[k / 2].y : dl[k / 2].x, e = k & 1 ? dp[k / 2].y : dp[k / 2].x;
+                const float duk = k & 1 ? du[k / 2].y : du[k / 2].x;
+                const float sdk = (k & 1 ? sd[k / 2].y : sd[k / 2].x) * 0.6931471805599453f;  // A was scaled by log2 e
+                T *px = Rows::row(xs, r, l) + ch, *pd = Rows::row(ds, r, l) + ch;
+                const float xv = ld_f32<T>(px);
+                float ddt = fmaf(xv, duk, sdk);
+                if (c.softplus) ddt *= sigmoid_f(ld_f32<T>(pd) + bias);
+                st_f32<T>(px, fmaf(d, duk, Dv * e));
+                st_f32<T>(pd, ddt);
+                dD = fmaf(e, xv, dD);
+                dbias += ddt;
+                if (c.z) {
+                    T *pz = Rows::row(zs, r, l) + ch;
+                    const float zv = ld_f32<T>(pz), sg = sigmoid_f(zv);
+                    const float pre = fmaf(Dv, xv, k & 1 ? p2[k / 2].y : p2[k / 2].x);
+                    st_f32<T>(pz, ld_f32<T>(Rows::row(ys, r, l) + ch) * pre * sg * fmaf(zv, 1.f - sg, 1.f));
+                }
+            }
+        }
+        __syncthreads();
+        const size_t row0 = (size_t)t0 * c.channels + c0;
+        Rows::flush(xs, static_cast<T *>(c.dx) + row0, c.channels, n, cols, len, wide);
+        Rows::flush(ds, static_cast<T *>(c.ddt) + row0, c.channels, n, cols, len, wide);
+        if (c.z) Rows::flush(zs, static_cast<T *>(c.dz) + row0, c.channels, n, cols, len, wide);
+        float *pb = parts.bc + ((size_t)blockIdx.y * c.seq.tokens + t0) * 2 * N;
+        for (int u = threadIdx.x; u < n * N; u += SEL_WARPS * 32) {
+            const int r = u / N, s = u - r * N, o = s * SEG + BC::at(r, len);
+            pb[r * 2 * N + s] = sB[o];
+            pb[r * 2 * N + N + s] = sC[o];
+        }
+    }
+    __syncthreads();
+    float *pa = parts.a + ((size_t)i * c.channels + c0) * N;
+    for (int u = threadIdx.x; u < cols * N; u += SEL_WARPS * 32) pa[u] = dAs[(u % N) * CB + u / N];
+#pragma unroll
+    for (int o = 1; o < TL; o *= 2) {
+        dD += __shfl_xor_sync(0xffffffffu, dD, o);
+        dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
+    }
+    if (l == 0 && ch < cols) {
+        float *pd = parts.d + (size_t)i * 2 * c.channels + c0 + ch;
+        pd[0] = dD;
+        pd[c.channels] = dbias;
+    }
+}
+
+// The sums over blocks.  The first row_blocks blocks: dB and dC, a warp per token,
+// from the channel tiles of each group; a token of no sequence gets zero gradients.
+// The others: dA, dD and dbias over the sequences, a thread per element.
+template <typename T>
+__global__ void __launch_bounds__(256) sel_bwd_sum(SelCall c, Parts parts, int row_blocks) {
+    const int N = c.dstate, G = c.groups, per_group = c.channels / G, tiles = (per_group + CB - 1) / CB;
+    if ((int)blockIdx.x < row_blocks) {
+        const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+        if (t >= c.seq.tokens) return;
+        int a = -1, b = c.seq.nseq;  // the last sequence that starts at or before t
+        while (b - a > 1) {
+            const int m = (a + b) >> 1;
+            if (c.seq.cu[m] <= t) a = m; else b = m;
+        }
+        const bool held = a >= 0 && c.seq.cu[a] >= 0 && t < c.seq.cu[a + 1] && c.seq.cu[a + 1] <= c.seq.tokens;
+        T *dB = static_cast<T *>(c.dB) + (size_t)t * G * N, *dC = static_cast<T *>(c.dC) + (size_t)t * G * N;
+        for (int u = lane; u < G * 2 * N; u += 32) {
+            const int g = u / (2 * N), k = u - g * 2 * N;
+            float s = 0.f;
+            if (held)
+                for (int j = 0; j < tiles; ++j) s += parts.bc[((size_t)(g * tiles + j) * c.seq.tokens + t) * 2 * N + k];
+            st_f32<T>(k < N ? dB + g * N + k : dC + g * N + k - N, s);
+        }
+        if (!held)
+            for (int d = lane; d < c.channels; d += 32) {
+                const size_t o = (size_t)t * c.channels + d;
+                st_f32<T>(static_cast<T *>(c.dx) + o, 0.f);
+                st_f32<T>(static_cast<T *>(c.ddt) + o, 0.f);
+                if (c.z) st_f32<T>(static_cast<T *>(c.dz) + o, 0.f);
+            }
+        return;
+    }
+    const long long u = (long long)(blockIdx.x - row_blocks) * 256 + threadIdx.x, na = (long long)c.channels * N;
+    if (u < na) {
+        float s = 0.f;
+        for (int i = 0; i < c.seq.nseq; ++i) s += parts.a[(size_t)i * na + u];
+        c.dA[u] = s;
+    } else if (u < na + 2 * c.channels) {
+        const long long v = u - na;
+        float s = 0.f;
+        for (int i = 0; i < c.seq.nseq; ++i) s += parts.d[(size_t)i * 2 * c.channels + v];
+        float *o = v < c.channels ? c.dD : c.dbias;
+        if (o) o[v < c.channels ? v : v - c.channels] = s;
+    }
+}
+
+size_t bc_floats(int tokens, int channels, int groups, int dstate) {
+    return (size_t)groups * ((channels / groups + CB - 1) / CB) * tokens * 2 * dstate;
+}
+
+template <typename T> cudaError_t run(const SelCall &c, float *ws, cudaStream_t st) {
+    using S = BwdShape<T>;
+    const size_t e = sizeof(T), smem = S::smem(c.dstate);
+    const int per_group = c.channels / c.groups;
+    const bool wide = rows_aligned(c.x, c.ld_x, e, 16) && rows_aligned(c.dt, c.ld_dt, e, 16) &&
+                      (!c.z || rows_aligned(c.z, c.ld_z, e, 16)) && c.channels * e % 16 == 0 && per_group * e % 16 == 0;
+    const bool wide_bc = c.dstate % 4 == 0 && rows_aligned(c.B, c.ld_b, e, 4 * e) && rows_aligned(c.C, c.ld_c, e, 4 * e);
+    Parts p;
+    p.bc = ws;
+    p.a = p.bc + bc_floats(c.seq.tokens, c.channels, c.groups, c.dstate);
+    p.d = p.a + (size_t)c.seq.nseq * c.channels * c.dstate;
+    if (c.seq.nseq > 0 && c.seq.tokens > 0) {
+        cudaError_t err = cudaFuncSetAttribute(sel_bwd_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (err != cudaSuccess) return err;
+        const dim3 grid(c.seq.nseq, c.groups * ((per_group + CB - 1) / CB));
+        sel_bwd_kernel<T><<<grid, SEL_WARPS * 32, smem, st>>>(c, p, wide, wide_bc);
+        err = cudaGetLastError();
+        if (err != cudaSuccess) return err;
+    }
+    SelCall s = c;
+    if (c.seq.tokens == 0) s.seq.nseq = 0;  // nothing was summed
+    const int row_blocks = (c.seq.tokens + 7) / 8;
+    const long long rest = ((long long)c.channels * (c.dstate + 2) + 255) / 256;
+    sel_bwd_sum<T><<<(unsigned)(row_blocks + rest), 256, 0, st>>>(s, p, row_blocks);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t sel_bwd_workspace(int tokens, int nseq, int channels, int groups, int dstate) {
+    return (bc_floats(tokens, channels, groups, dstate) + (size_t)nseq * channels * (dstate + 2)) * sizeof(float);
+}
+
+cudaError_t launch_sel_bwd(const SelCall &c, void *ws, cudaStream_t st) {
+    return c.bf16 ? run<__nv_bfloat16>(c, static_cast<float *>(ws), st) : run<float>(c, static_cast<float *>(ws), st);
+}
+
+}  // namespace ssd

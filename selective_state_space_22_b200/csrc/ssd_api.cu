@@ -12,6 +12,7 @@
 #include <string>
 
 #include "../../include/ssd.h"
+#include "mixer.cuh"
 #include "ssd_internal.cuh"
 
 // First device-side error raised by a kernel of this library on this device
@@ -287,6 +288,11 @@ bool valid_dtype(ssd_dtype d) { return d == SSD_F32 || d == SSD_BF16; }
 namespace ssd {
 void set_last_error(const char *msg) { g_last_error = msg; }
 
+int *device_error_word() {
+    ssd_status st = SSD_OK;
+    return device_error_ptr(&st);
+}
+
 void *current_context() {
     // cuCtxGetCurrent, fetched through the runtime so that libssd needs no link
     // against the driver library.
@@ -547,6 +553,9 @@ ssd_status ssd_get_device_status(void *stream) {
     if (code == ssd::DEV_TIMEOUT)
         return fail(SSD_ERR_TIMEOUT, "a bounded inter-block wait gave up on the device; the "
                     "outputs of the call that raised it are invalid");
+    if (code == ssd::DEV_BAD_INDEX)
+        return fail(SSD_ERR_INVALID_ARG, "sequence bounds or slot numbers in device memory were out of range, or a "
+                    "slot was named twice in one call; the sequences concerned were skipped");
     return fail(SSD_ERR_CUDA, "device error code %d", code);
 }
 

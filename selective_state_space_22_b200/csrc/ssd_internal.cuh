@@ -63,7 +63,7 @@ struct ScanArgs {
 };
 
 // Device error codes written to *dev_error (first writer wins).
-enum : int { DEV_OK = 0, DEV_TIMEOUT = 1 };
+enum : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_BAD_INDEX = 2 };
 
 // --------------------------------------------------------- kernel launchers
 // Each returns cudaSuccess or the launch error; none synchronises.

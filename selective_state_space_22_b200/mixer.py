@@ -1,0 +1,463 @@
+"""The rest of a mixer block around its matrix products: the short causal
+convolution and the gated Mamba-1 scan on packed prompts and on single tokens,
+their gradients, and the norms before and after the block.
+
+The functions have the C entry points' names (``include/ssd.h`` says what each
+argument means) and marshal arguments like the rest of the package.  Inputs that a
+projection's output holds side by side may be passed as slices: rows may be
+strided, the last dimension may not.  Outputs and scratch are allocated for each
+call on the stream that the call runs on, so calls on several streams and captured
+graphs never share scratch.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+_VP, _I, _LL, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.c_float
+_IO = {torch.float32: 0, torch.bfloat16: 1}
+_f32 = torch.float32
+
+
+class _SelArgs(ctypes.Structure):
+    _fields_ = ([(k, _VP) for k in ("x", "dt", "z", "B", "C", "A", "D", "dt_bias")]
+                + [(k, _LL) for k in ("x_stride", "dt_stride", "z_stride", "b_stride", "c_stride")]
+                + [(k, _I) for k in ("io_dtype", "softplus", "channels", "ngroups", "dstate")])
+
+
+def declare_mixer(lib):
+    def sig(name, *args, res=_I):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = args, res
+
+    sel = ctypes.POINTER(_SelArgs)
+    sig("ssd_conv1d_varlen", _VP, _LL, *[_VP] * 9, *[_I] * 8, _VP)
+    sig("ssd_conv1d_update", _VP, _VP, _VP, _LL, *[_VP] * 5, *[_I] * 7, _VP)
+    sig("ssd_conv1d_bwd_workspace_size", _I, _I, _I, res=_SZ)
+    sig("ssd_conv1d_bwd", _VP, _LL, *[_VP] * 9, *[_I] * 7, _VP, _SZ, _VP)
+    sig("ssd_selective_scan_chunk_states", _I, _I, res=_SZ)
+    sig("ssd_selective_scan_varlen", sel, *[_VP] * 6, _I, _I, _I, _VP)
+    sig("ssd_selective_state_update", sel, _VP, _VP, _VP, _I, _I, _VP)
+    sig("ssd_selective_scan_bwd_workspace_size", *[_I] * 5, res=_SZ)
+    sig("ssd_selective_scan_bwd", sel, *[_VP] * 11, _I, _I, _VP, _SZ, _VP)
+    sig("ssd_residual_rmsnorm", _VP, _LL, _VP, _LL, *[_VP] * 4, *[_I] * 4, _F, _VP)
+    sig("ssd_gated_rmsnorm", _VP, _LL, _VP, _LL, _VP, _LL, *[_VP] * 3, *[_I] * 5, _F, _VP)
+    sig("ssd_rmsnorm_bwd_workspace_size", _I, _I, res=_SZ)
+    sig("ssd_residual_rmsnorm_bwd", _VP, _LL, *[_VP] * 4, _LL, *[_VP] * 5, *[_I] * 4, _F, _VP, _SZ, _VP)
+    sig("ssd_gated_rmsnorm_bwd", _VP, _LL, _VP, _LL, *[_VP] * 7, *[_I] * 5, _F, _VP, _SZ, _VP)
+
+
+_same = contextlib.nullcontext()
+
+
+def _on(dev, stream):
+    """Makes the call's device and stream current where they are not."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return _same if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _lib_and_check():
+    from . import _check, load_library
+    return load_library(), _check
+
+
+def _io_of(t, name):
+    io = _IO.get(t.dtype)
+    if io is None:
+        raise ValueError(f"{name} must be bfloat16 or float32")
+    return io
+
+
+def _whole(t, name, dtype, dev, shape):
+    """Data pointer of a contiguous tensor, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
+        _explain(t, name, dtype, dev, shape)
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _explain(t, name, dtype, dev, shape):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _rows(t, name, dtype, dev, shape):
+    """(data pointer, row stride) of rows whose inner dimensions are contiguous."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype or t.device != dev or t.shape != shape:
+        _explain(t, name, dtype, dev, shape)
+    width, inner = 1, True
+    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        inner &= size == 1 or step == width
+        width *= size
+    ld = t.stride(0)
+    if not inner or (t.shape[0] > 1 and ld < width):
+        raise ValueError(f"{name}: the dimensions after the first must be contiguous and rows must not overlap")
+    return t.data_ptr(), max(ld, width)
+
+
+def _required(**tensors):
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is required")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        dev = dev or t.device
+    return dev
+
+
+def _need_dim(t, name, n):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
+
+
+def _sequences(cu_seqlens, dev):
+    if cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be a vector of the sequences' bounds")
+    nseq = cu_seqlens.numel() - 1
+    return _whole(cu_seqlens, "cu_seqlens", torch.int32, dev, (nseq + 1,)), nseq
+
+
+def _scratch(nbytes, dev):
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+
+
+def _size(n, what):
+    from . import SSD_WORKSPACE_INVALID, SSDError
+    if n == SSD_WORKSPACE_INVALID:
+        raise SSDError(1, f"invalid sizes for {what}")
+    return n
+
+
+def _fresh(out, name, shape, dtype, dev):
+    """out[name] checked, or a new tensor put there."""
+    t = out.get(name)
+    if t is None:
+        t = out[name] = torch.empty(shape, dtype=dtype, device=dev)
+        return t.data_ptr()
+    return _whole(t, name, dtype, dev, shape)
+
+
+# ------------------------------------------------------------------ convolution
+
+def _conv_outputs(out, n, x_channels, bc_channels, like):
+    shapes = ((n, x_channels), (n, bc_channels), (n, bc_channels))
+    if out is None:
+        out = tuple(torch.empty(s, dtype=like.dtype, device=like.device) for s in shapes)
+    return out, [_whole(t, name, like.dtype, like.device, s) for t, name, s in zip(out, ("x", "B", "C"), shapes)]
+
+
+def _conv_inputs(xbc, weight, bias, x_channels, bc_channels):
+    dev = _required(xbc=xbc, weight=weight)
+    _need_dim(xbc, "xbc", 2)
+    _need_dim(weight, "weight", 2)
+    n, ct = xbc.shape
+    if x_channels is None:
+        x_channels = ct - 2 * bc_channels
+    if ct != x_channels + 2 * bc_channels:
+        raise ValueError("xbc width must be x_channels + 2 bc_channels")
+    width = weight.shape[1]
+    return (dev, _io_of(xbc, "xbc"), n, x_channels, width, *_rows(xbc, "xbc", xbc.dtype, dev, (n, ct)),
+            _whole(weight, "weight", _f32, dev, (ct, width)), _whole(bias, "bias", _f32, dev, (ct,)))
+
+
+def ssd_conv1d_varlen(xbc, weight, bias, cu_seqlens, *, x_channels=None, bc_channels=0, silu=True, conv_state=None,
+                      slots=None, has_init=None, out=None, stream=None):
+    """The causal depthwise conv over packed prompts, split into the scan's inputs.
+
+    xbc [tokens, Cx+2Cb] bf16/float32 (rows may be strided), weight [Cx+2Cb, K] and
+    bias [Cx+2Cb] (or None) float32, cu_seqlens [nseq+1] int32.  conv_state [nslots,
+    Cx+2Cb, K-1] is read where has_init (bool [nseq]) says so and left holding each
+    prompt's last inputs, in slot slots[i] (int32 [nseq]; None: i).  Returns (x
+    [tokens, Cx], B, C [tokens, Cb]); rows of no sequence are left as they were."""
+    lib, check = _lib_and_check()
+    dev, io, n, x_channels, width, xp, ld, wp, bp = _conv_inputs(xbc, weight, bias, x_channels, bc_channels)
+    cu, nseq = _sequences(cu_seqlens, dev)
+    ct, nslots = xbc.shape[1], 0
+    if conv_state is not None:
+        _need_dim(conv_state, "conv_state", 3)
+        nslots = conv_state.shape[0]
+    sp = _whole(conv_state, "conv_state", xbc.dtype, dev, (nslots, ct, width - 1))
+    if sp == 0:  # no entries to keep (width 1, or no slots)
+        sp = None
+    slp = _whole(slots, "slots", torch.int32, dev, (nseq,))
+    hip = _whole(has_init, "has_init", torch.bool, dev, (nseq,))
+    with _on(dev, stream):
+        out, (xo, bo, co) = _conv_outputs(out, n, x_channels, bc_channels, xbc)
+        check(lib.ssd_conv1d_varlen(xp, ld, wp, bp, cu, sp, slp, hip, xo, bo or None, co or None, io, n, nseq, nslots,
+                                    x_channels, bc_channels, width, bool(silu), torch.cuda.current_stream(dev).cuda_stream))
+    return out
+
+
+def ssd_conv1d_update(conv_state, xbc, weight, bias=None, *, slots=None, x_channels=None, bc_channels=0, silu=True,
+                      out=None, stream=None):
+    """The conv of one new token per sequence; conv_state [nslots, Cx+2Cb, K-1] moves
+    on in place.  xbc [b, Cx+2Cb] (rows may be strided); sequence i uses slot slots[i]
+    (None: i), and a negative slot skips it.  Returns (x [b, Cx], B, C [b, Cb])."""
+    lib, check = _lib_and_check()
+    dev, io, n, x_channels, width, xp, ld, wp, bp = _conv_inputs(xbc, weight, bias, x_channels, bc_channels)
+    _required(xbc=xbc, conv_state=conv_state)
+    _need_dim(conv_state, "conv_state", 3)
+    nslots = conv_state.shape[0]
+    sp = _whole(conv_state, "conv_state", xbc.dtype, dev, (nslots, xbc.shape[1], width - 1))
+    slp = _whole(slots, "slots", torch.int32, dev, (n,))
+    with _on(dev, stream):
+        out, (xo, bo, co) = _conv_outputs(out, n, x_channels, bc_channels, xbc)
+        check(lib.ssd_conv1d_update(sp, slp, xp, ld, wp, bp, xo, bo or None, co or None, io, n, nslots, x_channels,
+                                    bc_channels, width, bool(silu), torch.cuda.current_stream(dev).cuda_stream))
+    return out
+
+
+def ssd_conv1d_bwd(xbc, weight, bias, cu_seqlens, dx, dB=None, dC=None, *, silu=True, out=None, stream=None):
+    """Gradients of ssd_conv1d_varlen without states: dict of dxbc [tokens, Cx+2Cb],
+    dweight and dbias (float32; dbias None when bias is); ``out`` may pass them
+    preallocated."""
+    lib, check = _lib_and_check()
+    _required(xbc=xbc, dx=dx)
+    _need_dim(dx, "dx", 2)
+    cb = 0 if dB is None else dB.shape[-1]
+    dev, io, n, cx, width, xp, ld, wp, bp = _conv_inputs(xbc, weight, bias, dx.shape[1], cb)
+    if cb and dC is None:
+        raise ValueError("dC is required")
+    cu, nseq = _sequences(cu_seqlens, dev)
+    ct = xbc.shape[1]
+    gx = _whole(dx, "dx", xbc.dtype, dev, (n, cx))
+    gb, gc = (_whole(t, k, xbc.dtype, dev, (n, cb)) if cb else None for t, k in ((dB, "dB"), (dC, "dC")))
+    with _on(dev, stream):
+        out = {} if out is None else out
+        po = [_fresh(out, "dxbc", (n, ct), xbc.dtype, dev), _fresh(out, "dweight", (ct, width), _f32, dev),
+              None if bias is None else _fresh(out, "dbias", (ct,), _f32, dev)]
+        out.setdefault("dbias", None)
+        nbytes = _size(lib.ssd_conv1d_bwd_workspace_size(n, ct, width), "the conv's gradient")
+        ws = _scratch(nbytes, dev)
+        check(lib.ssd_conv1d_bwd(xp, ld, wp, bp, cu, gx, gb, gc, *po, io, n, nseq, cx, cb, width, bool(silu),
+                                 None if ws is None else ws.data_ptr(), nbytes, torch.cuda.current_stream(dev).cuda_stream))
+    return out
+
+
+# --------------------------------------------------------------- selective scan
+
+def _sel_args(x, dt, A, B, C, D, z, dt_bias, softplus):
+    dev = _required(x=x, dt=dt, A=A, B=B, C=C)
+    _need_dim(x, "x", 2)
+    _need_dim(B, "B", 3)
+    (n, d), (_, G, N), io = x.shape, B.shape, x.dtype
+    a = _SelArgs()
+    a.io_dtype = _io_of(x, "x")
+    a.x, a.x_stride = _rows(x, "x", io, dev, (n, d))
+    a.dt, a.dt_stride = _rows(dt, "dt", io, dev, (n, d))
+    a.z, a.z_stride = _rows(z, "z", io, dev, (n, d))
+    a.B, a.b_stride = _rows(B, "B", io, dev, (n, G, N))
+    a.C, a.c_stride = _rows(C, "C", io, dev, (n, G, N))
+    a.A = _whole(A, "A", _f32, dev, (d, N))
+    a.D = _whole(D, "D", _f32, dev, (d,))
+    a.dt_bias = _whole(dt_bias, "dt_bias", _f32, dev, (d,))
+    a.softplus, a.channels, a.ngroups, a.dstate = bool(softplus), d, G, N
+    return a, dev, n, d, G, N
+
+
+def _states(state, slots, rows, d, N, dev):
+    _need_dim(state, "state", 3)
+    nslots = state.shape[0]
+    return _whole(state, "state", _f32, dev, (nslots, d, N)), _whole(slots, "slots", torch.int32, dev, (rows,)), nslots
+
+
+def ssd_selective_scan_varlen(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, *, softplus=True, state=None,
+                              slots=None, has_init=None, y=None, return_chunk_states=False, stream=None):
+    """The gated Mamba-1 scan over packed prompts.  Returns (y, chunk_states or None).
+
+    x, dt, z [tokens, channels] and B, C [tokens, G, N], one dtype (bf16/float32), rows
+    may be strided; A [channels, N], D, dt_bias [channels] float32; cu_seqlens [nseq+1]
+    int32.  dt is before the bias and the softplus.  state [nslots, channels, N]
+    float32 is read where has_init (bool [nseq]) says so and left holding each
+    prompt's end state, in slot slots[i] (int32; None: i).  return_chunk_states keeps
+    what ssd_selective_scan_bwd needs."""
+    lib, check = _lib_and_check()
+    a, dev, n, d, _, N = _sel_args(x, dt, A, B, C, D, z, dt_bias, softplus)
+    cu, nseq = _sequences(cu_seqlens, dev)
+    sp = slp = None
+    nslots = 0
+    if state is not None:
+        sp, slp, nslots = _states(state, slots, nseq, d, N, dev)
+    hip = _whole(has_init, "has_init", torch.bool, dev, (nseq,))
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty((n, d), dtype=x.dtype, device=dev)
+        kept = None
+        if return_chunk_states:
+            kept = torch.empty((_size(lib.ssd_selective_scan_chunk_states(n, nseq), "the scan"), d, N), dtype=_f32, device=dev)
+        check(lib.ssd_selective_scan_varlen(a, cu, sp, slp, hip, None if kept is None else kept.data_ptr(),
+                                            _whole(y, "y", x.dtype, dev, (n, d)), n, nseq, nslots,
+                                            torch.cuda.current_stream(dev).cuda_stream))
+    return y, kept
+
+
+def ssd_selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, *, softplus=True, slots=None, y=None,
+                               stream=None):
+    """One token per sequence of the gated Mamba-1 scan; ``state`` [nslots, channels, N]
+    float32 is updated in place.  x, dt, z [b, channels], B, C [b, G, N] (rows may be
+    strided); sequence i uses slot slots[i] (None: i), and a negative slot skips it.
+    Returns y [b, channels]."""
+    lib, check = _lib_and_check()
+    a, dev, n, d, _, N = _sel_args(x, dt, A, B, C, D, z, dt_bias, softplus)
+    _required(x=x, state=state)
+    sp, slp, nslots = _states(state, slots, n, d, N, dev)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty((n, d), dtype=x.dtype, device=dev)
+        check(lib.ssd_selective_state_update(a, sp, slp, _whole(y, "y", x.dtype, dev, (n, d)), n, nslots,
+                                             torch.cuda.current_stream(dev).cuda_stream))
+    return y
+
+
+def ssd_selective_scan_bwd(x, dt, A, B, C, cu_seqlens, dy, chunk_states, D=None, z=None, dt_bias=None, *, softplus=True,
+                           out=None, stream=None):
+    """Gradients of ssd_selective_scan_varlen without states, from dy and the forward's
+    chunk_states: dict of dx, ddt, dz, dB, dC (io dtype) and dA, dD, ddt_bias (float32);
+    those of absent inputs are None.  ``out`` may pass them preallocated."""
+    lib, check = _lib_and_check()
+    a, dev, n, d, G, N = _sel_args(x, dt, A, B, C, D, z, dt_bias, softplus)
+    cu, nseq = _sequences(cu_seqlens, dev)
+    _required(dy=dy, chunk_states=chunk_states)
+    gy = _whole(dy, "dy", x.dtype, dev, (n, d))
+    kept = _whole(chunk_states, "chunk_states", _f32, dev, (_size(lib.ssd_selective_scan_chunk_states(n, nseq), "the scan"), d, N))
+    with _on(dev, stream):
+        out = {} if out is None else out
+        shapes = dict(dx=((n, d), x.dtype, x), ddt=((n, d), x.dtype, dt), dz=((n, d), x.dtype, z), dB=((n, G, N), x.dtype, B),
+                      dC=((n, G, N), x.dtype, C), dA=((d, N), _f32, A), dD=((d,), _f32, D), ddt_bias=((d,), _f32, dt_bias))
+        po = [None if of is None else _fresh(out, k, s, t, dev) for k, (s, t, of) in shapes.items()]
+        for k in shapes:
+            out.setdefault(k, None)
+        nbytes = _size(lib.ssd_selective_scan_bwd_workspace_size(n, nseq, d, G, N), "the scan's gradient")
+        ws = _scratch(nbytes, dev)
+        check(lib.ssd_selective_scan_bwd(a, cu, gy, kept, *po, n, nseq, None if ws is None else ws.data_ptr(), nbytes,
+                                         torch.cuda.current_stream(dev).cuda_stream))
+    return out
+
+
+# ------------------------------------------------------------------------ norms
+
+def ssd_residual_rmsnorm(x, weight, residual=None, scale=None, *, eps=1e-5, out=None, residual_out=None, stream=None):
+    """r = residual + scale * x and out = rmsnorm(r) * weight, before a block.
+
+    x [rows, width] bf16/float32, residual of x's dtype or float32 (rows of both may
+    be strided), scale and weight [width] float32.  Returns (out, r): r in the
+    residual's dtype (x's when there is none; residual_out may be residual itself)."""
+    lib, check = _lib_and_check()
+    dev = _required(x=x, weight=weight)
+    _need_dim(x, "x", 2)
+    n, d = x.shape
+    rt = x.dtype if residual is None else residual.dtype
+    if rt not in (x.dtype, _f32):
+        raise ValueError("residual must have x's dtype or float32")
+    io = _io_of(x, "x")
+    xp, ldx = _rows(x, "x", x.dtype, dev, (n, d))
+    rp, ldr = _rows(residual, "residual", rt, dev, (n, d))
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((n, d), dtype=x.dtype, device=dev)
+        if residual_out is None:
+            residual_out = torch.empty((n, d), dtype=rt, device=dev)
+        check(lib.ssd_residual_rmsnorm(xp, ldx, rp, ldr, _whole(scale, "scale", _f32, dev, (d,)),
+                                       _whole(weight, "weight", _f32, dev, (d,)), _whole(out, "out", x.dtype, dev, (n, d)),
+                                       _whole(residual_out, "residual_out", rt, dev, (n, d)), io, _IO[rt], n, d, eps,
+                                       torch.cuda.current_stream(dev).cuda_stream))
+    return out, residual_out
+
+
+def ssd_residual_rmsnorm_bwd(residual, weight, dout, dresidual=None, x=None, scale=None, *, eps=1e-5, out=None, stream=None):
+    """Gradients of ssd_residual_rmsnorm from the r it returned: dict of dresidual (r's
+    dtype), dx (dout's dtype; the same tensor where neither scale nor a wider dtype
+    sets them apart), dweight, and dscale (None without scale, which needs x)."""
+    lib, check = _lib_and_check()
+    dev = _required(residual=residual, weight=weight, dout=dout)
+    _need_dim(residual, "residual", 2)
+    (n, d), rt, t = residual.shape, residual.dtype, dout.dtype
+    io = _io_of(dout, "dout")
+    if rt not in (t, _f32):
+        raise ValueError("residual must have dout's dtype or float32")
+    if scale is not None and x is None:
+        raise ValueError("x is required with scale")
+    rp, ldr = _rows(residual, "residual", rt, dev, (n, d))
+    xp, ldx = _rows(x, "x", t, dev, (n, d)) if scale is not None else (None, 0)
+    with _on(dev, stream):
+        out = {} if out is None else out
+        gr, apart = _fresh(out, "dresidual", (n, d), rt, dev), scale is not None or rt != t
+        gx = _fresh(out, "dx", (n, d), t, dev) if apart else None
+        if not apart:
+            out["dx"] = out["dresidual"]
+        gw = _fresh(out, "dweight", (d,), _f32, dev)
+        gs = None if scale is None else _fresh(out, "dscale", (d,), _f32, dev)
+        out.setdefault("dscale", None)
+        nbytes = _size(lib.ssd_rmsnorm_bwd_workspace_size(n, d), "the norm's gradient")
+        ws = _scratch(nbytes, dev)
+        check(lib.ssd_residual_rmsnorm_bwd(rp, ldr, _whole(weight, "weight", _f32, dev, (d,)), _whole(dout, "dout", t, dev, (n, d)),
+                                           _whole(dresidual, "dresidual", rt, dev, (n, d)), xp, ldx,
+                                           _whole(scale, "scale", _f32, dev, (d,)), gx, gr, gw, gs, io, _IO[rt], n, d, eps,
+                                           None if ws is None else ws.data_ptr(), nbytes,
+                                           torch.cuda.current_stream(dev).cuda_stream))
+    return out
+
+
+def ssd_gated_rmsnorm(y, z, weight, residual=None, scale=None, *, ngroups=1, norm_before_gate=False, eps=1e-5, out=None,
+                      stream=None):
+    """rmsnorm(y * silu(z)) * weight over each of ngroups groups of channels, or
+    rmsnorm(y) * weight * silu(z) with norm_before_gate; times scale and plus residual
+    where they are given.  y, z (None: no gate), residual [rows, width] of one dtype
+    (bf16/float32; rows may be strided), weight, scale [width] float32."""
+    lib, check = _lib_and_check()
+    dev = _required(y=y, weight=weight)
+    _need_dim(y, "y", 2)
+    n, d = y.shape
+    io = _io_of(y, "y")
+    yp, ldy = _rows(y, "y", y.dtype, dev, (n, d))
+    zp, ldz = _rows(z, "z", y.dtype, dev, (n, d))
+    rp, ldr = _rows(residual, "residual", y.dtype, dev, (n, d))
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((n, d), dtype=y.dtype, device=dev)
+        check(lib.ssd_gated_rmsnorm(yp, ldy, zp, ldz, rp, ldr, _whole(scale, "scale", _f32, dev, (d,)),
+                                    _whole(weight, "weight", _f32, dev, (d,)), _whole(out, "out", y.dtype, dev, (n, d)), io, n, d,
+                                    ngroups, bool(norm_before_gate), eps, torch.cuda.current_stream(dev).cuda_stream))
+    return out
+
+
+def ssd_gated_rmsnorm_bwd(y, z, weight, dout, scale=None, *, ngroups=1, norm_before_gate=False, eps=1e-5, out=None,
+                          stream=None):
+    """Gradients of ssd_gated_rmsnorm: dict of dy, dz (None without z), dweight and
+    dscale (None without scale); the residual's gradient is dout."""
+    lib, check = _lib_and_check()
+    dev = _required(y=y, weight=weight, dout=dout)
+    _need_dim(y, "y", 2)
+    n, d = y.shape
+    io = _io_of(y, "y")
+    yp, ldy = _rows(y, "y", y.dtype, dev, (n, d))
+    zp, ldz = _rows(z, "z", y.dtype, dev, (n, d))
+    with _on(dev, stream):
+        out = {} if out is None else out
+        gy, gz = _fresh(out, "dy", (n, d), y.dtype, dev), None if z is None else _fresh(out, "dz", (n, d), y.dtype, dev)
+        gw = _fresh(out, "dweight", (d,), _f32, dev)
+        gs = None if scale is None else _fresh(out, "dscale", (d,), _f32, dev)
+        out.setdefault("dz", None)
+        out.setdefault("dscale", None)
+        nbytes = _size(lib.ssd_rmsnorm_bwd_workspace_size(n, d), "the norm's gradient")
+        ws = _scratch(nbytes, dev)
+        check(lib.ssd_gated_rmsnorm_bwd(yp, ldy, zp, ldz, _whole(weight, "weight", _f32, dev, (d,)),
+                                        _whole(dout, "dout", y.dtype, dev, (n, d)), _whole(scale, "scale", _f32, dev, (d,)), gy, gz, gw, gs,
+                                        io, n, d, ngroups, bool(norm_before_gate), eps,
+                                        None if ws is None else ws.data_ptr(), nbytes,
+                                        torch.cuda.current_stream(dev).cuda_stream))
+    return out
