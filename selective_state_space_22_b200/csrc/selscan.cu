@@ -22,6 +22,82 @@ template <typename T, int TL, int K> struct FwdShape {
     static size_t smem(int N) { return 3 * (size_t)Rows::BYTES + (size_t)N * BC::STATE_WORDS * 4 + 2 * (size_t)CB * N * 4; }
 };
 
+// One chunk: the lane's tokens (4 Q slots, `mine` of them real) of channel ch, over
+// all states.  Q is a compile-time number so that the arrays stay in registers and
+// the state loop has no branches.
+template <typename T, int TL, int K, int Q>
+__device__ __forceinline__ void fwd_chunk(const SelCall &c, unsigned char *xs, unsigned char *ds, unsigned char *zs,
+                                          const uint32_t *bc, const float *As, float *hs, int l, int ch, int mine, float bias,
+                                          float Dv) {
+    using S = FwdShape<T, TL, K>;
+    using Rows = typename S::Rows;
+    using BC = typename S::BC;
+    constexpr int CB = S::CB, LEN = 4 * Q;
+    const int N = c.dstate;
+    float2 dl[LEN / 2], u2[LEN / 2], y2[LEN / 2];
+    float total = 0.f;
+#pragma unroll
+    for (int k = 0; k < LEN; ++k) {
+        float d = 0.f, u = 0.f;
+        if (k < mine) {
+            d = ld_f32<T>(Rows::row(ds, l * LEN + k, l) + ch) + bias;
+            if (c.softplus) d = softplus_f(d);
+            u = d * ld_f32<T>(Rows::row(xs, l * LEN + k, l) + ch);
+        }
+        total += d;
+        if (k & 1)
+            dl[k / 2].y = d, u2[k / 2].y = u;
+        else
+            dl[k / 2].x = d, u2[k / 2].x = u;
+    }
+#pragma unroll
+    for (int k = 0; k < LEN / 2; ++k) y2[k] = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int s = 0; s < N; ++s) {
+        const float A2 = As[s * CB + ch], hc = hs[s * CB + ch];
+        const float2 A22 = splat(A2);
+        float2 a2[LEN / 2], b2[LEN / 2], c2[LEN / 2];
+        float S_ = 0.f, P = ex2a(A2 * total);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            BC::quad(bc, s, q, l, b2 + 2 * q, c2 + 2 * q);
+#pragma unroll
+            for (int k = 2 * q; k < 2 * q + 2; ++k) {
+                const float2 arg = mul2(dl[k], A22);
+                a2[k] = make_float2(ex2a(arg.x), ex2a(arg.y));
+                b2[k] = mul2(u2[k], b2[k]);
+                S_ = fmaf(a2[k].x, S_, b2[k].x);
+                S_ = fmaf(a2[k].y, S_, b2[k].y);
+            }
+        }
+        if (l == 0) S_ = fmaf(P, hc, S_);
+#pragma unroll
+        for (int o = 1; o < TL; o *= 2) {
+            const float Sp = __shfl_up_sync(0xffffffffu, S_, o, TL), Pp = __shfl_up_sync(0xffffffffu, P, o, TL);
+            if (l >= o) S_ = fmaf(P, Sp, S_), P *= Pp;
+        }
+        float h = __shfl_up_sync(0xffffffffu, S_, 1, TL);
+        if (l == 0) h = hc;
+        if (l == TL - 1) hs[s * CB + ch] = S_;
+#pragma unroll
+        for (int k = 0; k < LEN / 2; ++k) {
+            float2 hh;
+            hh.x = h = fmaf(a2[k].x, h, b2[k].x);
+            hh.y = h = fmaf(a2[k].y, h, b2[k].y);
+            y2[k] = fma2(c2[k], hh, y2[k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < LEN; ++k) {
+        if (k < mine) {
+            T *px = Rows::row(xs, l * LEN + k, l) + ch;
+            float o = fmaf(Dv, ld_f32<T>(px), k & 1 ? y2[k / 2].y : y2[k / 2].x);
+            if (c.z) o *= silu_v(ld_f32<T>(Rows::row(zs, l * LEN + k, l) + ch));
+            st_f32<T>(px, o);
+        }
+    }
+}
+
 template <typename T, int TL, int K>
 __global__ void __launch_bounds__(SEL_WARPS * 32, 2) sel_fwd_kernel(SelCall c, bool wide, bool wide_bc) {
     using S = FwdShape<T, TL, K>;
@@ -72,76 +148,11 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, 2) sel_fwd_kernel(SelCall c, b
             __syncthreads();  // before hs moves on
         }
         const int mine = ch < cols ? max(0, min(len, n - l * len)) : 0;  // tokens of this lane
-        float2 dl[K / 2], u2[K / 2], y2[K / 2];
-        float total = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float d = 0.f, u = 0.f;
-            if (k < mine) {
-                d = ld_f32<T>(Rows::row(ds, l * len + k, l) + ch) + bias;
-                if (c.softplus) d = softplus_f(d);
-                u = d * ld_f32<T>(Rows::row(xs, l * len + k, l) + ch);
-            }
-            total += d;
-            if (k & 1)
-                dl[k / 2].y = d, u2[k / 2].y = u;
-            else
-                dl[k / 2].x = d, u2[k / 2].x = u;
-        }
-#pragma unroll
-        for (int k = 0; k < K / 2; ++k) y2[k] = make_float2(0.f, 0.f);
-#pragma unroll 1
-        for (int s = 0; s < N; ++s) {
-            const float A2 = As[s * CB + ch], hc = hs[s * CB + ch];
-            const float2 A22 = splat(A2);
-            float2 a2[K / 2], b2[K / 2], c2[K / 2];
-            float S_ = 0.f, P = ex2a(A2 * total);
-#pragma unroll
-            for (int q = 0; q < K / 4; ++q) {
-                if (4 * q >= len) break;
-                float b[4], cv[4];
-                BC::quad(bc, s, q, l, b, cv);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int k = 2 * q + j;
-                    const float2 arg = mul2(dl[k], A22);
-                    a2[k] = make_float2(ex2a(arg.x), ex2a(arg.y));
-                    b2[k] = mul2(u2[k], make_float2(b[2 * j], b[2 * j + 1]));
-                    c2[k] = make_float2(cv[2 * j], cv[2 * j + 1]);
-                    S_ = fmaf(a2[k].x, S_, b2[k].x);
-                    S_ = fmaf(a2[k].y, S_, b2[k].y);
-                }
-            }
-            if (l == 0) S_ = fmaf(P, hc, S_);
-#pragma unroll
-            for (int o = 1; o < TL; o *= 2) {
-                const float Sp = __shfl_up_sync(0xffffffffu, S_, o, TL), Pp = __shfl_up_sync(0xffffffffu, P, o, TL);
-                if (l >= o) S_ = fmaf(P, Sp, S_), P *= Pp;
-            }
-            float h = __shfl_up_sync(0xffffffffu, S_, 1, TL);
-            if (l == 0) h = hc;
-            if (l == TL - 1) hs[s * CB + ch] = S_;
-#pragma unroll
-            for (int q = 0; q < K / 4; ++q) {
-                if (4 * q >= len) break;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int k = 2 * q + j;
-                    float2 hh;
-                    hh.x = h = fmaf(a2[k].x, h, b2[k].x);
-                    hh.y = h = fmaf(a2[k].y, h, b2[k].y);
-                    y2[k] = fma2(c2[k], hh, y2[k]);
-                }
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (k < mine) {
-                T *px = Rows::row(xs, l * len + k, l) + ch;
-                float o = fmaf(Dv, ld_f32<T>(px), k & 1 ? y2[k / 2].y : y2[k / 2].x);
-                if (c.z) o *= silu_v(ld_f32<T>(Rows::row(zs, l * len + k, l) + ch));
-                st_f32<T>(px, o);
-            }
+        switch (len / 4) {
+        case 1: fwd_chunk<T, TL, K, 1>(c, xs, ds, zs, bc, As, hs, l, ch, mine, bias, Dv); break;
+        case 2: fwd_chunk<T, TL, K, 2>(c, xs, ds, zs, bc, As, hs, l, ch, mine, bias, Dv); break;
+        case 3: fwd_chunk<T, TL, K, 3>(c, xs, ds, zs, bc, As, hs, l, ch, mine, bias, Dv); break;
+        default: fwd_chunk<T, TL, K, 4>(c, xs, ds, zs, bc, As, hs, l, ch, mine, bias, Dv); break;
         }
         __syncthreads();
         Rows::flush(xs, y + (size_t)t0 * c.channels, c.channels, n, cols, len, wide);

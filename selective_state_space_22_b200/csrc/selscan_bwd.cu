@@ -37,6 +37,174 @@ struct Parts {      // workspace
     float *d;       // [nseq][2][channels]: dD, dbias
 };
 
+// Where a lane stands and what its block holds in shared memory.
+struct Lane {
+    int l, cl, ch, w;    // lane run, channel of the warp, channel of the block, warp
+    int mine;            // real tokens of the run
+    float bias, D;
+    unsigned char *xs, *ds, *zs, *ys;
+    const uint32_t *bc;
+    const float *As, *hs;
+    float *gs, *dAs, *sB, *sC;
+};
+
+// One chunk of 4 Q token slots per lane run: on return the tiles x, dt, z hold dx,
+// ddt, dz.  dD and dbias go on in the lane's registers.
+template <typename T, int Q>
+__device__ __forceinline__ void bwd_chunk(const SelCall &c, const Lane &a, float &dD, float &dbias) {
+    using Rows = typename BwdShape<T>::Rows;
+    using BC = typename BwdShape<T>::BC;
+    constexpr int LEN = 4 * Q, H = LEN / 2;
+    const int N = c.dstate, M = max(N, SEL_WARPS), l = a.l, ch = a.ch;
+    float2 dl[H], u2[H], dp[H], du[H], sd[H], p2[H];
+    float total = 0.f;
+#pragma unroll
+    for (int k = 0; k < LEN; ++k) {
+        float d = 0.f, u = 0.f, e = 0.f;
+        if (k < a.mine) {
+            const int r = l * LEN + k;
+            d = ld_f32<T>(Rows::row(a.ds, r, l) + ch) + a.bias;
+            if (c.softplus) d = softplus_f(d);
+            u = d * ld_f32<T>(Rows::row(a.xs, r, l) + ch);
+            e = ld_f32<T>(Rows::row(a.ys, r, l) + ch);
+            if (c.z) e *= silu_v(ld_f32<T>(Rows::row(a.zs, r, l) + ch));
+        }
+        total += d;
+        if (k & 1)
+            dl[k / 2].y = d, u2[k / 2].y = u, dp[k / 2].y = e;
+        else
+            dl[k / 2].x = d, u2[k / 2].x = u, dp[k / 2].x = e;
+    }
+#pragma unroll
+    for (int k = 0; k < H; ++k) du[k] = sd[k] = p2[k] = make_float2(0.f, 0.f);
+    // Sum of v over the warp's channels: lane cl ends with tokens 4 cl .. 4 cl + 3
+    // of its run, which it adds to the block's sums.
+    auto reduce = [&](const float2 (&v)[H], float *acc) {
+        float v8[8], sum[4];
+        const float2 none = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // cl bit 1: the run's halves
+            const float2 first = k < H ? v[k < H ? k : 0] : none, second = k + 4 < H ? v[k + 4 < H ? k + 4 : 0] : none;
+            const float2 keep = a.cl & 2 ? second : first, give = a.cl & 2 ? first : second;
+            v8[2 * k] = keep.x + __shfl_xor_sync(0xffffffffu, give.x, 2 * TL);
+            v8[2 * k + 1] = keep.y + __shfl_xor_sync(0xffffffffu, give.y, 2 * TL);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // cl bit 0: quads
+            const float keep = a.cl & 1 ? v8[k + 4] : v8[k], give = a.cl & 1 ? v8[k] : v8[k + 4];
+            sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, TL);
+        }
+        if (a.cl < Q) {
+            float4 *o = reinterpret_cast<float4 *>(acc + (a.cl * TL + l) * 4);
+            float4 t = *o;
+            t.x += sum[0], t.y += sum[1], t.z += sum[2], t.w += sum[3];
+            *o = t;
+        }
+    };
+#pragma unroll 1
+    for (int it = 0; it < M; ++it) {
+        const int s = it + a.w < M ? it + a.w : it + a.w - M;
+        if (s < N) {
+            const float A2 = a.As[s * CB + ch], hc = a.hs[s * CB + ch], gc = a.gs[s * CB + ch];
+            const float2 A22 = splat(A2);
+            float2 a2[H], hp[H], v2[H], b2[H], c2[H];
+            // forwards: v2 holds the inputs, then dp h
+            float S_ = 0.f, P = ex2a(A2 * total);
+            const float P0 = P;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                BC::quad(a.bc, s, q, l, b2 + 2 * q, c2 + 2 * q);
+#pragma unroll
+                for (int k = 2 * q; k < 2 * q + 2; ++k) {
+                    const float2 arg = mul2(dl[k], A22);
+                    a2[k] = make_float2(ex2a(arg.x), ex2a(arg.y));
+                    v2[k] = mul2(u2[k], b2[k]);
+                    S_ = fmaf(a2[k].x, S_, v2[k].x);
+                    S_ = fmaf(a2[k].y, S_, v2[k].y);
+                }
+            }
+            if (l == 0) S_ = fmaf(P, hc, S_);
+#pragma unroll
+            for (int o = 1; o < TL; o *= 2) {
+                const float Sp = __shfl_up_sync(0xffffffffu, S_, o, TL), Pp = __shfl_up_sync(0xffffffffu, P, o, TL);
+                if (l >= o) S_ = fmaf(P, Sp, S_), P *= Pp;
+            }
+            float h = __shfl_up_sync(0xffffffffu, S_, 1, TL);
+            if (l == 0) h = hc;
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                float2 hh;
+                hp[k].x = h;
+                hh.x = h = fmaf(a2[k].x, h, v2[k].x);
+                hp[k].y = h;
+                hh.y = h = fmaf(a2[k].y, h, v2[k].y);
+                p2[k] = fma2(c2[k], hh, p2[k]);
+                v2[k] = mul2(dp[k], hh);
+            }
+            reduce(v2, a.sC + s * SEG);
+            // backwards: G = a g, what a token hands to the one before it
+            float R = 0.f;
+            P = P0;
+#pragma unroll
+            for (int k = H - 1; k >= 0; --k) {
+                v2[k] = mul2(dp[k], c2[k]);
+                R = a2[k].y * (R + v2[k].y);
+                R = a2[k].x * (R + v2[k].x);
+            }
+            if (l == TL - 1) R = fmaf(P, gc, R);
+#pragma unroll
+            for (int o = 1; o < TL; o *= 2) {
+                const float Rn = __shfl_down_sync(0xffffffffu, R, o, TL), Pn = __shfl_down_sync(0xffffffffu, P, o, TL);
+                if (l + o < TL) R = fmaf(P, Rn, R), P *= Pn;
+            }
+            float G = __shfl_down_sync(0xffffffffu, R, 1, TL);
+            if (l == TL - 1) G = gc;
+            if (l == 0) a.gs[s * CB + ch] = R;
+            float2 dA2 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = H - 1; k >= 0; --k) {
+                float2 gg, GG;
+                gg.y = G + v2[k].y, GG.y = G = a2[k].y * gg.y;
+                gg.x = G + v2[k].x, GG.x = G = a2[k].x * gg.x;
+                const float2 qq = mul2(GG, hp[k]);
+                du[k] = fma2(gg, b2[k], du[k]);
+                sd[k] = fma2(A22, qq, sd[k]);
+                dA2 = fma2(dl[k], qq, dA2);
+                v2[k] = mul2(u2[k], gg);
+            }
+            reduce(v2, a.sB + s * SEG);
+            float dA = dA2.x + dA2.y;
+#pragma unroll
+            for (int o = 1; o < TL; o *= 2) dA += __shfl_xor_sync(0xffffffffu, dA, o);
+            if (l == 0) a.dAs[s * CB + ch] += dA;
+        }
+        __syncthreads();  // the next state's sums
+    }
+#pragma unroll
+    for (int k = 0; k < LEN; ++k) {
+        if (k < a.mine) {
+            const int r = l * LEN + k;
+            const float d = k & 1 ? dl[k / 2].y : dl[k / 2].x, e = k & 1 ? dp[k / 2].y : dp[k / 2].x;
+            const float duk = k & 1 ? du[k / 2].y : du[k / 2].x;
+            const float sdk = (k & 1 ? sd[k / 2].y : sd[k / 2].x) * 0.6931471805599453f;  // A was scaled by log2 e
+            T *px = Rows::row(a.xs, r, l) + ch, *pd = Rows::row(a.ds, r, l) + ch;
+            const float xv = ld_f32<T>(px);
+            float ddt = fmaf(xv, duk, sdk);
+            if (c.softplus) ddt *= sigmoid_f(ld_f32<T>(pd) + a.bias);
+            st_f32<T>(px, fmaf(d, duk, a.D * e));
+            st_f32<T>(pd, ddt);
+            dD = fmaf(e, xv, dD);
+            dbias += ddt;
+            if (c.z) {
+                T *pz = Rows::row(a.zs, r, l) + ch;
+                const float zv = ld_f32<T>(pz), sg = sigmoid_f(zv);
+                const float pre = fmaf(a.D, xv, k & 1 ? p2[k / 2].y : p2[k / 2].x);
+                st_f32<T>(pz, ld_f32<T>(Rows::row(a.ys, r, l) + ch) * pre * sg * fmaf(zv, 1.f - sg, 1.f));
+            }
+        }
+    }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(SEL_WARPS * 32, 1) sel_bwd_kernel(SelCall c, Parts parts, bool wide, bool wide_bc) {
     using S = BwdShape<T>;
@@ -67,7 +235,8 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, 1) sel_bwd_kernel(SelCall c, P
         gs[n * CB + cc] = dAs[n * CB + cc] = 0.f;
     }
     float dD = 0.f, dbias = 0.f;
-    const int chunks = (hi - lo + SEG - 1) / SEG, M = max(N, SEL_WARPS);
+    Lane at{l, cl, ch, w, 0, bias, Dv, xs, ds, zs, ys, bc, As, hs, gs, dAs, sB, sC};
+    const int chunks = (hi - lo + SEG - 1) / SEG;
     for (int chunk = chunks - 1; chunk >= 0; --chunk) {
         const int t0 = lo + chunk * SEG, n = min(SEG, hi - t0), len = ((n + TL - 1) / TL + 3) & ~3;
         __syncthreads();  // the tiles are free again
@@ -83,185 +252,12 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, 1) sel_bwd_kernel(SelCall c, P
         for (int u = threadIdx.x; u < N * SEG; u += SEL_WARPS * 32) sB[u] = sC[u] = 0.f;
         cp_wait<0>();
         __syncthreads();
-        const int mine = ch < cols ? max(0, min(len, n - l * len)) : 0;
-        float2 dl[K / 2], u2[K / 2], dp[K / 2], du[K / 2], sd[K / 2], p2[K / 2];
-        float total = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float d = 0.f, u = 0.f, e = 0.f;
-            if (k < mine) {
-                const int r = l * len + k;
-                d = ld_f32<T>(Rows::row(ds, r, l) + ch) + bias;
-                if (c.softplus) d = softplus_f(d);
-                u = d * ld_f32<T>(Rows::row(xs, r, l) + ch);
-                e = ld_f32<T>(Rows::row(ys, r, l) + ch);
-                if (c.z) e *= silu_v(ld_f32<T>(Rows::row(zs, r, l) + ch));
-            }
-            total += d;
-            if (k & 1)
-                dl[k / 2].y = d, u2[k / 2].y = u, dp[k / 2].y = e;
-            else
-                dl[k / 2].x = d, u2[k / 2].x = u, dp[k / 2].x = e;
-        }
-#pragma unroll
-        for (int k = 0; k < K / 2; ++k) du[k] = sd[k] = p2[k] = make_float2(0.f, 0.f);
-#pragma unroll 1
-        for (int it = 0; it < M; ++it) {
-            const int s = it + w < M ? it + w : it + w - M;
-            if (s < N) {
-                const float A2 = As[s * CB + ch], hc = hs[s * CB + ch], gc = gs[s * CB + ch];
-                const float2 A22 = splat(A2);
-                float2 a2[K / 2], hp[K / 2], v2[K / 2];
-                // forwards: v2 holds the inputs, then dp h
-                float S_ = 0.f, P = ex2a(A2 * total);
-                const float P0 = P;
-#pragma unroll
-                for (int q = 0; q < K / 4; ++q) {
-                    if (4 * q >= len) break;
-                    float b[4], cv[4];
-                    BC::quad(bc, s, q, l, b, cv);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int k = 2 * q + j;
-                        const float2 arg = mul2(dl[k], A22);
-                        a2[k] = make_float2(ex2a(arg.x), ex2a(arg.y));
-                        v2[k] = mul2(u2[k], make_float2(b[2 * j], b[2 * j + 1]));
-                        S_ = fmaf(a2[k].x, S_, v2[k].x);
-                        S_ = fmaf(a2[k].y, S_, v2[k].y);
-                    }
-                }
-                if (l == 0) S_ = fmaf(P, hc, S_);
-#pragma unroll
-                for (int o = 1; o < TL; o *= 2) {
-                    const float Sp = __shfl_up_sync(0xffffffffu, S_, o, TL), Pp = __shfl_up_sync(0xffffffffu, P, o, TL);
-                    if (l >= o) S_ = fmaf(P, Sp, S_), P *= Pp;
-                }
-                float h = __shfl_up_sync(0xffffffffu, S_, 1, TL);
-                if (l == 0) h = hc;
-                float R = 0.f;
-#pragma unroll
-                for (int q = 0; q < K / 4; ++q) {
-                    if (4 * q >= len) break;
-                    float b[4], cv[4];
-                    BC::quad(bc, s, q, l, b, cv);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int k = 2 * q + j;
-                        float2 hh;
-                        hp[k].x = h;
-                        hh.x = h = fmaf(a2[k].x, h, v2[k].x);
-                        hp[k].y = h;
-                        hh.y = h = fmaf(a2[k].y, h, v2[k].y);
-                        p2[k] = fma2(make_float2(cv[2 * j], cv[2 * j + 1]), hh, p2[k]);
-                        v2[k] = mul2(dp[k], hh);
-                    }
-                }
-                // dC of the warp's channels: lane cl ends with tokens 4 cl .. 4 cl + 3
-                float sum[4];
-                auto reduce = [&] {
-                    float v8[8];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {  // cl bit 1: the run's halves
-                        const float2 keep = cl & 2 ? v2[k + 4] : v2[k], give = cl & 2 ? v2[k] : v2[k + 4];
-                        v8[2 * k] = keep.x + __shfl_xor_sync(0xffffffffu, give.x, 2 * TL);
-                        v8[2 * k + 1] = keep.y + __shfl_xor_sync(0xffffffffu, give.y, 2 * TL);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {  // cl bit 0: quads
-                        const float keep = cl & 1 ? v8[k + 4] : v8[k], give = cl & 1 ? v8[k] : v8[k + 4];
-                        sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, TL);
-                    }
-                };
-                auto add_to = [&](float *acc) {
-                    float4 *o = reinterpret_cast<float4 *>(acc + s * SEG + (cl * TL + l) * 4);
-                    float4 v = *o;
-                    v.x += sum[0], v.y += sum[1], v.z += sum[2], v.w += sum[3];
-                    *o = v;
-                };
-                if (len < K)
-#pragma unroll
-                    for (int k = 0; k < K / 2; ++k)
-                        if (2 * k >= len) v2[k] = make_float2(0.f, 0.f);
-                reduce();
-                if (4 * cl < len) add_to(sC);
-                // backwards: G = a g, what a token hands to the one before it
-                P = P0;
-#pragma unroll
-                for (int q = K / 4 - 1; q >= 0; --q) {
-                    if (4 * q >= len) continue;
-                    float b[4], cv[4];
-                    BC::quad(bc, s, q, l, b, cv);
-#pragma unroll
-                    for (int j = 1; j >= 0; --j) {
-                        const int k = 2 * q + j;
-                        v2[k] = mul2(dp[k], make_float2(cv[2 * j], cv[2 * j + 1]));
-                        R = a2[k].y * (R + v2[k].y);
-                        R = a2[k].x * (R + v2[k].x);
-                    }
-                }
-                if (l == TL - 1) R = fmaf(P, gc, R);
-#pragma unroll
-                for (int o = 1; o < TL; o *= 2) {
-                    const float Rn = __shfl_down_sync(0xffffffffu, R, o, TL), Pn = __shfl_down_sync(0xffffffffu, P, o, TL);
-                    if (l + o < TL) R = fmaf(P, Rn, R), P *= Pn;
-                }
-                float G = __shfl_down_sync(0xffffffffu, R, 1, TL);
-                if (l == TL - 1) G = gc;
-                if (l == 0) gs[s * CB + ch] = R;
-                float2 dA2 = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int q = K / 4 - 1; q >= 0; --q) {
-                    if (4 * q >= len) continue;
-                    float b[4], cv[4];
-                    BC::quad(bc, s, q, l, b, cv);
-#pragma unroll
-                    for (int j = 1; j >= 0; --j) {
-                        const int k = 2 * q + j;
-                        float2 gg, GG;
-                        gg.y = G + v2[k].y, GG.y = G = a2[k].y * gg.y;
-                        gg.x = G + v2[k].x, GG.x = G = a2[k].x * gg.x;
-                        const float2 qq = mul2(GG, hp[k]);
-                        du[k] = fma2(gg, make_float2(b[2 * j], b[2 * j + 1]), du[k]);
-                        sd[k] = fma2(A22, qq, sd[k]);
-                        dA2 = fma2(dl[k], qq, dA2);
-                        v2[k] = mul2(u2[k], gg);
-                    }
-                }
-                if (len < K)
-#pragma unroll
-                    for (int k = 0; k < K / 2; ++k)
-                        if (2 * k >= len) v2[k] = make_float2(0.f, 0.f);
-                reduce();
-                if (4 * cl < len) add_to(sB);
-                float dA = dA2.x + dA2.y;
-#pragma unroll
-                for (int o = 1; o < TL; o *= 2) dA += __shfl_xor_sync(0xffffffffu, dA, o);
-                if (l == 0) dAs[s * CB + ch] += dA;
-            }
-            __syncthreads();  // the next state's sums
-        }
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (k < mine) {
-                const int r = l * len + k;
-                const float d = k & 1 ? dl[k / 2].y : dl[k / 2].x, e = k & 1 ? dp[k / 2].y : dp[k / 2].x;
-                const float duk = k & 1 ? du[k / 2].y : du[k / 2].x;
-                const float sdk = (k & 1 ? sd[k / 2].y : sd[k / 2].x) * 0.6931471805599453f;  // A was scaled by log2 e
-                T *px = Rows::row(xs, r, l) + ch, *pd = Rows::row(ds, r, l) + ch;
-                const float xv = ld_f32<T>(px);
-                float ddt = fmaf(xv, duk, sdk);
-                if (c.softplus) ddt *= sigmoid_f(ld_f32<T>(pd) + bias);
-                st_f32<T>(px, fmaf(d, duk, Dv * e));
-                st_f32<T>(pd, ddt);
-                dD = fmaf(e, xv, dD);
-                dbias += ddt;
-                if (c.z) {
-                    T *pz = Rows::row(zs, r, l) + ch;
-                    const float zv = ld_f32<T>(pz), sg = sigmoid_f(zv);
-                    const float pre = fmaf(Dv, xv, k & 1 ? p2[k / 2].y : p2[k / 2].x);
-                    st_f32<T>(pz, ld_f32<T>(Rows::row(ys, r, l) + ch) * pre * sg * fmaf(zv, 1.f - sg, 1.f));
-                }
-            }
+        at.mine = ch < cols ? max(0, min(len, n - l * len)) : 0;
+        switch (len / 4) {
+        case 1: bwd_chunk<T, 1>(c, at, dD, dbias); break;
+        case 2: bwd_chunk<T, 2>(c, at, dD, dbias); break;
+        case 3: bwd_chunk<T, 3>(c, at, dD, dbias); break;
+        default: bwd_chunk<T, 4>(c, at, dD, dbias); break;
         }
         __syncthreads();
         const size_t row0 = (size_t)t0 * c.channels + c0;

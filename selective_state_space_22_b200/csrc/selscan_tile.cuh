@@ -104,18 +104,19 @@ template <typename T, int SEG, int TL> struct BCTile {
             }
         }
     }
-    // B and C of quad q of lane run l for state s.
-    static __device__ __forceinline__ void quad(const uint32_t *bc, int s, int q, int l, float (&b)[4], float (&c)[4]) {
+    // B and C of quad q of lane run l for state s, as two pairs of tokens each.
+    static __device__ __forceinline__ void quad(const uint32_t *bc, int s, int q, int l, float2 *b, float2 *c) {
         const uint32_t *p = bc + s * STATE_WORDS + (q * TL + l) * 4;
         if constexpr (PACK) {
             const uint4 v = *reinterpret_cast<const uint4 *>(p);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[i] = __uint_as_float(w[i] << 16), c[i] = __uint_as_float(w[i] & 0xffff0000u);
+            b[0] = make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.y << 16));
+            b[1] = make_float2(__uint_as_float(v.z << 16), __uint_as_float(v.w << 16));
+            c[0] = make_float2(__uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y & 0xffff0000u));
+            c[1] = make_float2(__uint_as_float(v.z & 0xffff0000u), __uint_as_float(v.w & 0xffff0000u));
         } else {
             const float4 v = *reinterpret_cast<const float4 *>(p), u = *reinterpret_cast<const float4 *>(p + SEG);
-            b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
-            c[0] = u.x, c[1] = u.y, c[2] = u.z, c[3] = u.w;
+            b[0] = make_float2(v.x, v.y), b[1] = make_float2(v.z, v.w);
+            c[0] = make_float2(u.x, u.y), c[1] = make_float2(u.z, u.w);
         }
     }
 };
