@@ -63,13 +63,28 @@ __device__ __forceinline__ float ex2a(float v) {  // 2^v, relative error about 2
 }
 constexpr float LOG2E = 1.4426950408889634f;
 
-// 1 / (1 + e^-v).  The exponent is capped so that the divisor stays below 2^126,
-// where the fast divide is exact to 2 ulp; past the cap the value is below 1e-34.
-__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.f, 1.f + __expf(fminf(-v, 80.f))); }
+__device__ __forceinline__ float rcpa(float v) {  // 1/v, 1 ulp; subnormal results are zero
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// 1 / (1 + e^-v): past v = -88 the exponential is infinite and the result zero
+// (its value there is below 1e-38).
+__device__ __forceinline__ float sigmoid_f(float v) { return rcpa(1.f + ex2a(-LOG2E * v)); }
 __device__ __forceinline__ float silu_v(float v) { return v * sigmoid_f(v); }
-// ln(1 + e^v) = max(v, 0) + ln(1 + e^-|v|): no overflow, and small steps (v far
-// below zero) keep their relative precision.
-__device__ __forceinline__ float softplus_f(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+// ln(1 + e^v) = max(v, 0) + ln(1 + t), t = e^-|v|: no overflow, and small steps (v
+// far below zero) keep their relative precision.  ln(1 + t) = 2 artanh(s) with
+// s = t / (2 + t) <= 1/3, by artanh's series: seven terms leave 1.4e-8.
+__device__ __forceinline__ float softplus_f(float v) {
+    const float t = ex2a(-LOG2E * fabsf(v)), s = t * rcpa(2.f + t), q = s * s;
+    float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
+    p = fmaf(q, p, 1.f / 9.f);
+    p = fmaf(q, p, 1.f / 7.f);
+    p = fmaf(q, p, 1.f / 5.f);
+    p = fmaf(q, p, 1.f / 3.f);
+    p = fmaf(q, p, 1.f);
+    return fmaf(2.f * s, p, fmaxf(v, 0.f));
+}
 
 // ------------------------------------------------------------- packed pairs
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -87,7 +102,19 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
         : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
     return *reinterpret_cast<float2 *>(&r);
 }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ float2 silu2(float2 v) {
+    const float2 e = mul2(v, splat(-LOG2E)), d = add2(make_float2(ex2a(e.x), ex2a(e.y)), splat(1.f));
+    return mul2(v, make_float2(rcpa(d.x), rcpa(d.y)));
+}
 
 // V consecutive elements <-> floats, one access of V * sizeof(T) bytes where WIDE
 // (the caller has checked the alignment), else V accesses.
@@ -101,6 +128,9 @@ template <typename T, int V, bool WIDE> __device__ __forceinline__ void load_v(c
         const uint2 q = *reinterpret_cast<const uint2 *>(p);
         v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
         v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
+    } else if constexpr (WIDE && sizeof(T) == 4 && V == 2) {
+        const float2 q = *reinterpret_cast<const float2 *>(p);
+        v[0] = q.x, v[1] = q.y;
     } else if constexpr (WIDE && sizeof(T) == 4 && V % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < V; i += 4) {
@@ -122,6 +152,8 @@ template <typename T, int V, bool WIDE> __device__ __forceinline__ void store_v(
             make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     } else if constexpr (WIDE && sizeof(T) == 2 && V == 4) {
         *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    } else if constexpr (WIDE && sizeof(T) == 4 && V == 2) {
+        *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
     } else if constexpr (WIDE && sizeof(T) == 4 && V % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);

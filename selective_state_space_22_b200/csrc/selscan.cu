@@ -163,57 +163,72 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, 2) sel_fwd_kernel(SelCall c, b
 }
 
 // One token per sequence, in place on the state.  LP lanes share a channel, four
-// states each (dstate = 4 LP), so a warp reads and writes whole lines of the
-// state; LP = 0: any dstate, a lane per channel.  Bound by HBM: the state in and out.
+// states each (dstate = 4 LP), so a warp reads and writes whole lines of the state; a
+// thread takes U channels, a block's stride apart, with all its loads first.
+// LP = 0: any dstate, a lane per channel.  Bound by HBM: the state in and out.
 constexpr int UPD_THREADS = 256;
-template <typename T, int LP>
+template <typename T, int LP, int U>
 __global__ void __launch_bounds__(UPD_THREADS) sel_update_kernel(SelCall c, bool wide_bc) {
-    const int i = blockIdx.y, slot = slot_of(c.seq.slots, c.seq.nslots, i, c.seq.dev_error);
-    if (slot < 0) return;
-    constexpr int L = LP ? LP : 1;
-    const int d = (blockIdx.x * UPD_THREADS + threadIdx.x) / L, q = threadIdx.x % L, N = c.dstate;
-    const bool in = d < c.channels;
-    const int dc = in ? d : c.channels - 1, g = dc / (c.channels / c.groups);
-    const size_t row = ((size_t)slot * c.channels + dc) * N;
-    const T *B = static_cast<const T *>(c.B) + i * c.ld_b + g * N, *C = static_cast<const T *>(c.C) + i * c.ld_c + g * N;
-    float4 h = make_float4(0.f, 0.f, 0.f, 0.f), a = h;
-    if constexpr (LP > 0) {  // the wide loads first
-        h = __ldcs(reinterpret_cast<const float4 *>(c.state + row) + q);
-        a = __ldg(reinterpret_cast<const float4 *>(c.A + (size_t)dc * N) + q);
-    }
-    const float xv = ld_f32<T>(static_cast<const T *>(c.x) + i * c.ld_x + dc);
-    float delta = ld_f32<T>(static_cast<const T *>(c.dt) + i * c.ld_dt + dc) + (c.dt_bias ? c.dt_bias[dc] : 0.f);
-    const float zv = c.z ? ld_f32<T>(static_cast<const T *>(c.z) + i * c.ld_z + dc) : 0.f;
-    const float Dv = c.D ? c.D[dc] : 0.f;
-    if (c.softplus) delta = softplus_f(delta);
-    const float u = delta * xv, d2 = delta * LOG2E;
-    float acc = 0.f;
-    if constexpr (LP > 0) {
-        float b[4], cv[4];
-        if (wide_bc) {
-            load_v<T, 4, true>(B + 4 * q, b), load_v<T, 4, true>(C + 4 * q, cv);
-        } else {
-            load_v<T, 4, false>(B + 4 * q, b), load_v<T, 4, false>(C + 4 * q, cv);
-        }
-        h.x = fmaf(ex2a(d2 * a.x), h.x, u * b[0]);
-        h.y = fmaf(ex2a(d2 * a.y), h.y, u * b[1]);
-        h.z = fmaf(ex2a(d2 * a.z), h.z, u * b[2]);
-        h.w = fmaf(ex2a(d2 * a.w), h.w, u * b[3]);
-        acc = fmaf(cv[0], h.x, fmaf(cv[1], h.y, fmaf(cv[2], h.z, cv[3] * h.w)));
-        if (in) __stcs(reinterpret_cast<float4 *>(c.state + row) + q, h);
+    constexpr int L = LP ? LP : 1, CH = UPD_THREADS / L;  // channels per block and step
+    const int i = blockIdx.y, N = c.dstate, q = threadIdx.x % L, per_group = c.channels / c.groups;
+    const int d0 = blockIdx.x * CH * U + threadIdx.x / L;
+    // everything that does not depend on the slot is on its way while the slot is looked up
+    float xv[U], dt[U], zv[U], bias[U], Dv[U];
+    float4 a[U];
 #pragma unroll
-        for (int o = 1; o < L; o *= 2) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    } else if (in) {
-        for (int n = 0; n < N; ++n) {
-            const float hn = fmaf(ex2a(d2 * c.A[(size_t)dc * N + n]), c.state[row + n], u * ld_f32<T>(B + n));
-            c.state[row + n] = hn;
-            acc = fmaf(ld_f32<T>(C + n), hn, acc);
-        }
+    for (int u = 0; u < U; ++u) {
+        const int d = min(d0 + u * CH, c.channels - 1);
+        xv[u] = ld_f32<T>(static_cast<const T *>(c.x) + i * c.ld_x + d);
+        dt[u] = ld_f32<T>(static_cast<const T *>(c.dt) + i * c.ld_dt + d);
+        zv[u] = c.z ? ld_f32<T>(static_cast<const T *>(c.z) + i * c.ld_z + d) : 0.f;
+        bias[u] = c.dt_bias ? c.dt_bias[d] : 0.f;
+        Dv[u] = c.D ? c.D[d] : 0.f;
+        if constexpr (LP > 0) a[u] = __ldg(reinterpret_cast<const float4 *>(c.A + (size_t)d * N) + q);
     }
-    if (in && q == 0) {
-        float o = fmaf(Dv, xv, acc);
-        if (c.z) o *= silu_v(zv);
-        st_f32<T>(static_cast<T *>(c.y) + (size_t)i * c.channels + d, o);
+    const int slot = slot_of(c.seq.slots, c.seq.nslots, i, c.seq.dev_error);
+    if (slot < 0) return;
+    float *st = c.state + (size_t)slot * c.channels * N;
+    float4 h[U];
+    if constexpr (LP > 0)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            h[u] = __ldcs(reinterpret_cast<const float4 *>(st + (size_t)min(d0 + u * CH, c.channels - 1) * N) + q);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int d = d0 + u * CH;
+        const bool in = d < c.channels;
+        const int g = min(d, c.channels - 1) / per_group;
+        const T *B = static_cast<const T *>(c.B) + i * c.ld_b + g * N, *C = static_cast<const T *>(c.C) + i * c.ld_c + g * N;
+        float delta = dt[u] + bias[u], acc = 0.f;
+        if (c.softplus) delta = softplus_f(delta);
+        const float du = delta * xv[u], d2 = delta * LOG2E;
+        if constexpr (LP > 0) {
+            float b[4], cv[4];
+            if (wide_bc) {
+                load_v<T, 4, true>(B + 4 * q, b), load_v<T, 4, true>(C + 4 * q, cv);
+            } else {
+                load_v<T, 4, false>(B + 4 * q, b), load_v<T, 4, false>(C + 4 * q, cv);
+            }
+            h[u].x = fmaf(ex2a(d2 * a[u].x), h[u].x, du * b[0]);
+            h[u].y = fmaf(ex2a(d2 * a[u].y), h[u].y, du * b[1]);
+            h[u].z = fmaf(ex2a(d2 * a[u].z), h[u].z, du * b[2]);
+            h[u].w = fmaf(ex2a(d2 * a[u].w), h[u].w, du * b[3]);
+            acc = fmaf(cv[0], h[u].x, fmaf(cv[1], h[u].y, fmaf(cv[2], h[u].z, cv[3] * h[u].w)));
+            if (in) __stcs(reinterpret_cast<float4 *>(st + (size_t)d * N) + q, h[u]);
+#pragma unroll
+            for (int o = 1; o < L; o *= 2) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+        } else if (in) {
+            for (int n = 0; n < N; ++n) {
+                float *hn = st + (size_t)d * N + n;
+                *hn = fmaf(ex2a(d2 * c.A[(size_t)d * N + n]), *hn, du * ld_f32<T>(B + n));
+                acc = fmaf(ld_f32<T>(C + n), *hn, acc);
+            }
+        }
+        if (in && q == 0) {
+            float o = fmaf(Dv[u], xv[u], acc);
+            if (c.z) o *= silu_v(zv[u]);
+            st_f32<T>(static_cast<T *>(c.y) + (size_t)i * c.channels + d, o);
+        }
     }
 }
 
@@ -238,12 +253,17 @@ template <typename T> cudaError_t pick_fwd(const SelCall &c, cudaStream_t st) {
     return run_fwd<T, 8, 16>(c, st);
 }
 
+template <typename T, int LP, int U> cudaError_t run_update(const SelCall &c, int batch, bool wide_bc, cudaStream_t st) {
+    const int per = UPD_THREADS / (LP ? LP : 1) * U;
+    sel_update_kernel<T, LP, U><<<dim3((c.channels + per - 1) / per, batch), UPD_THREADS, 0, st>>>(c, wide_bc);
+    return cudaGetLastError();
+}
+// Four channels per thread once that still leaves every SM eight blocks.
 template <typename T, int LP> cudaError_t run_update(const SelCall &c, int batch, cudaStream_t st) {
     const size_t e = sizeof(T);
     const bool wide_bc = rows_aligned(c.B, c.ld_b, e, 4 * e) && rows_aligned(c.C, c.ld_c, e, 4 * e);
-    const int per = UPD_THREADS / (LP ? LP : 1);
-    sel_update_kernel<T, LP><<<dim3((c.channels + per - 1) / per, batch), UPD_THREADS, 0, st>>>(c, wide_bc);
-    return cudaGetLastError();
+    const long long blocks = (long long)batch * c.channels * (LP ? LP : 1) / (UPD_THREADS * 4);
+    return blocks >= 148 * 8 ? run_update<T, LP, 4>(c, batch, wide_bc, st) : run_update<T, LP, 1>(c, batch, wide_bc, st);
 }
 template <typename T> cudaError_t pick_update(const SelCall &c, int batch, cudaStream_t st) {
     switch (c.dstate) {

@@ -50,18 +50,32 @@ def declare_mixer(lib):
 
 
 _same = contextlib.nullcontext()
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream  # without the lazy-init wrappers
+_calls = {}
+
+
+def _call(name):
+    """The C function, and the function that turns its status into an exception."""
+    f = _calls.get(name)
+    if f is None:
+        from . import _check, load_library
+        f = _calls[name] = (getattr(load_library(), name), _check)
+    return f
 
 
 def _on(dev, stream):
     """Makes the call's device and stream current where they are not."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    return _same if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return _same if _device() == dev.index else torch.cuda.device(dev)
 
 
-def _lib_and_check():
-    from . import _check, load_library
-    return load_library(), _check
+def _device_of(t, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
 
 
 def _io_of(t, name):
@@ -72,16 +86,20 @@ def _io_of(t, name):
 
 
 def _whole(t, name, dtype, dev, shape):
-    """Data pointer of a contiguous tensor, or None."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
+    """Data pointer of a contiguous tensor."""
+    if t is None or t.dtype != dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
         _explain(t, name, dtype, dev, shape)
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
+def _maybe(t, name, dtype, dev, shape):
+    return None if t is None else _whole(t, name, dtype, dev, shape)
+
+
 def _explain(t, name, dtype, dev, shape):
+    if t is None:
+        raise ValueError(f"{name} is required")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device != dev:
@@ -94,29 +112,18 @@ def _explain(t, name, dtype, dev, shape):
 
 def _rows(t, name, dtype, dev, shape):
     """(data pointer, row stride) of rows whose inner dimensions are contiguous."""
-    if t is None:
-        return None, 0
-    if t.dtype != dtype or t.device != dev or t.shape != shape:
+    if t is None or t.dtype != dtype or t.device != dev or t.shape != shape:
         _explain(t, name, dtype, dev, shape)
-    width, inner = 1, True
-    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        inner &= size == 1 or step == width
-        width *= size
-    ld = t.stride(0)
-    if not inner or (t.shape[0] > 1 and ld < width):
+    width = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    step = t.stride()
+    inner = step[-1] == 1 or shape[-1] == 1
+    if len(shape) == 3:
+        inner &= step[1] == shape[2] or shape[1] == 1
+    if not inner or (shape[0] > 1 and step[0] < width):
         raise ValueError(f"{name}: the dimensions after the first must be contiguous and rows must not overlap")
-    return t.data_ptr(), max(ld, width)
-
-
-def _required(**tensors):
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            raise ValueError(f"{name} is required")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        dev = dev or t.device
-    return dev
+    return t.data_ptr(), max(step[0], width)
 
 
 def _need_dim(t, name, n):
@@ -125,9 +132,9 @@ def _need_dim(t, name, n):
 
 
 def _sequences(cu_seqlens, dev):
-    if cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+    if cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be a vector of the sequences' bounds")
-    nseq = cu_seqlens.numel() - 1
+    nseq = cu_seqlens.shape[0] - 1
     return _whole(cu_seqlens, "cu_seqlens", torch.int32, dev, (nseq + 1,)), nseq
 
 
@@ -135,10 +142,12 @@ def _scratch(nbytes, dev):
     return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
 
 
-def _size(n, what):
-    from . import SSD_WORKSPACE_INVALID, SSDError
-    if n == SSD_WORKSPACE_INVALID:
-        raise SSDError(1, f"invalid sizes for {what}")
+def _size(name, *sizes):
+    """What one of the C size functions answers."""
+    n = _call(name)[0](*sizes)
+    if n == (1 << 64) - 1:  # SSD_WORKSPACE_INVALID
+        from . import SSDError
+        raise SSDError(1, f"{name}: invalid sizes {sizes}")
     return n
 
 
@@ -154,14 +163,17 @@ def _fresh(out, name, shape, dtype, dev):
 # ------------------------------------------------------------------ convolution
 
 def _conv_outputs(out, n, x_channels, bc_channels, like):
-    shapes = ((n, x_channels), (n, bc_channels), (n, bc_channels))
+    sx, sb = (n, x_channels), (n, bc_channels)
     if out is None:
-        out = tuple(torch.empty(s, dtype=like.dtype, device=like.device) for s in shapes)
-    return out, [_whole(t, name, like.dtype, like.device, s) for t, name, s in zip(out, ("x", "B", "C"), shapes)]
+        out = (like.new_empty(sx), like.new_empty(sb), like.new_empty(sb))
+        return out, (out[0].data_ptr(), out[1].data_ptr() or None, out[2].data_ptr() or None)
+    io, dev = like.dtype, like.device
+    return out, (_whole(out[0], "x", io, dev, sx), _whole(out[1], "B", io, dev, sb) or None, _whole(out[2], "C", io, dev, sb) or None)
 
 
 def _conv_inputs(xbc, weight, bias, x_channels, bc_channels):
-    dev = _required(xbc=xbc, weight=weight)
+    dev = _device_of(xbc, "xbc")
+    _device_of(weight, "weight")
     _need_dim(xbc, "xbc", 2)
     _need_dim(weight, "weight", 2)
     n, ct = xbc.shape
@@ -170,8 +182,9 @@ def _conv_inputs(xbc, weight, bias, x_channels, bc_channels):
     if ct != x_channels + 2 * bc_channels:
         raise ValueError("xbc width must be x_channels + 2 bc_channels")
     width = weight.shape[1]
-    return (dev, _io_of(xbc, "xbc"), n, x_channels, width, *_rows(xbc, "xbc", xbc.dtype, dev, (n, ct)),
-            _whole(weight, "weight", _f32, dev, (ct, width)), _whole(bias, "bias", _f32, dev, (ct,)))
+    xp, ld = _rows(xbc, "xbc", xbc.dtype, dev, (n, ct))
+    return (dev, _io_of(xbc, "xbc"), n, ct, x_channels, width, xp, ld, _whole(weight, "weight", _f32, dev, (ct, width)),
+            _maybe(bias, "bias", _f32, dev, (ct,)))
 
 
 def ssd_conv1d_varlen(xbc, weight, bias, cu_seqlens, *, x_channels=None, bc_channels=0, silu=True, conv_state=None,
@@ -183,22 +196,20 @@ def ssd_conv1d_varlen(xbc, weight, bias, cu_seqlens, *, x_channels=None, bc_chan
     Cx+2Cb, K-1] is read where has_init (bool [nseq]) says so and left holding each
     prompt's last inputs, in slot slots[i] (int32 [nseq]; None: i).  Returns (x
     [tokens, Cx], B, C [tokens, Cb]); rows of no sequence are left as they were."""
-    lib, check = _lib_and_check()
-    dev, io, n, x_channels, width, xp, ld, wp, bp = _conv_inputs(xbc, weight, bias, x_channels, bc_channels)
+    f, check = _call("ssd_conv1d_varlen")
+    dev, io, n, ct, x_channels, width, xp, ld, wp, bp = _conv_inputs(xbc, weight, bias, x_channels, bc_channels)
     cu, nseq = _sequences(cu_seqlens, dev)
-    ct, nslots = xbc.shape[1], 0
+    sp, nslots = None, 0
     if conv_state is not None:
         _need_dim(conv_state, "conv_state", 3)
         nslots = conv_state.shape[0]
-    sp = _whole(conv_state, "conv_state", xbc.dtype, dev, (nslots, ct, width - 1))
-    if sp == 0:  # no entries to keep (width 1, or no slots)
-        sp = None
-    slp = _whole(slots, "slots", torch.int32, dev, (nseq,))
-    hip = _whole(has_init, "has_init", torch.bool, dev, (nseq,))
+        sp = _whole(conv_state, "conv_state", xbc.dtype, dev, (nslots, ct, width - 1)) or None
+    slp = _maybe(slots, "slots", torch.int32, dev, (nseq,))
+    hip = _maybe(has_init, "has_init", torch.bool, dev, (nseq,))
     with _on(dev, stream):
         out, (xo, bo, co) = _conv_outputs(out, n, x_channels, bc_channels, xbc)
-        check(lib.ssd_conv1d_varlen(xp, ld, wp, bp, cu, sp, slp, hip, xo, bo or None, co or None, io, n, nseq, nslots,
-                                    x_channels, bc_channels, width, bool(silu), torch.cuda.current_stream(dev).cuda_stream))
+        check(f(xp, ld, wp, bp, cu, sp, slp, hip, xo, bo, co, io, n, nseq, nslots, x_channels, bc_channels, width,
+                bool(silu), _raw_stream(dev.index)))
     return out
 
 
@@ -207,17 +218,17 @@ def ssd_conv1d_update(conv_state, xbc, weight, bias=None, *, slots=None, x_chann
     """The conv of one new token per sequence; conv_state [nslots, Cx+2Cb, K-1] moves
     on in place.  xbc [b, Cx+2Cb] (rows may be strided); sequence i uses slot slots[i]
     (None: i), and a negative slot skips it.  Returns (x [b, Cx], B, C [b, Cb])."""
-    lib, check = _lib_and_check()
-    dev, io, n, x_channels, width, xp, ld, wp, bp = _conv_inputs(xbc, weight, bias, x_channels, bc_channels)
-    _required(xbc=xbc, conv_state=conv_state)
+    f, check = _call("ssd_conv1d_update")
+    dev, io, n, ct, x_channels, width, xp, ld, wp, bp = _conv_inputs(xbc, weight, bias, x_channels, bc_channels)
+    _device_of(conv_state, "conv_state")
     _need_dim(conv_state, "conv_state", 3)
     nslots = conv_state.shape[0]
-    sp = _whole(conv_state, "conv_state", xbc.dtype, dev, (nslots, xbc.shape[1], width - 1))
-    slp = _whole(slots, "slots", torch.int32, dev, (n,))
+    sp = _whole(conv_state, "conv_state", xbc.dtype, dev, (nslots, ct, width - 1))
+    slp = _maybe(slots, "slots", torch.int32, dev, (n,))
     with _on(dev, stream):
         out, (xo, bo, co) = _conv_outputs(out, n, x_channels, bc_channels, xbc)
-        check(lib.ssd_conv1d_update(sp, slp, xp, ld, wp, bp, xo, bo or None, co or None, io, n, nslots, x_channels,
-                                    bc_channels, width, bool(silu), torch.cuda.current_stream(dev).cuda_stream))
+        check(f(sp, slp, xp, ld, wp, bp, xo, bo, co, io, n, nslots, x_channels, bc_channels, width, bool(silu),
+                _raw_stream(dev.index)))
     return out
 
 
@@ -225,15 +236,13 @@ def ssd_conv1d_bwd(xbc, weight, bias, cu_seqlens, dx, dB=None, dC=None, *, silu=
     """Gradients of ssd_conv1d_varlen without states: dict of dxbc [tokens, Cx+2Cb],
     dweight and dbias (float32; dbias None when bias is); ``out`` may pass them
     preallocated."""
-    lib, check = _lib_and_check()
-    _required(xbc=xbc, dx=dx)
+    f, check = _call("ssd_conv1d_bwd")
+    _device_of(xbc, "xbc")
+    _device_of(dx, "dx")
     _need_dim(dx, "dx", 2)
     cb = 0 if dB is None else dB.shape[-1]
-    dev, io, n, cx, width, xp, ld, wp, bp = _conv_inputs(xbc, weight, bias, dx.shape[1], cb)
-    if cb and dC is None:
-        raise ValueError("dC is required")
+    dev, io, n, ct, cx, width, xp, ld, wp, bp = _conv_inputs(xbc, weight, bias, dx.shape[1], cb)
     cu, nseq = _sequences(cu_seqlens, dev)
-    ct = xbc.shape[1]
     gx = _whole(dx, "dx", xbc.dtype, dev, (n, cx))
     gb, gc = (_whole(t, k, xbc.dtype, dev, (n, cb)) if cb else None for t, k in ((dB, "dB"), (dC, "dC")))
     with _on(dev, stream):
@@ -241,30 +250,34 @@ def ssd_conv1d_bwd(xbc, weight, bias, cu_seqlens, dx, dB=None, dC=None, *, silu=
         po = [_fresh(out, "dxbc", (n, ct), xbc.dtype, dev), _fresh(out, "dweight", (ct, width), _f32, dev),
               None if bias is None else _fresh(out, "dbias", (ct,), _f32, dev)]
         out.setdefault("dbias", None)
-        nbytes = _size(lib.ssd_conv1d_bwd_workspace_size(n, ct, width), "the conv's gradient")
+        nbytes = _size("ssd_conv1d_bwd_workspace_size", n, ct, width)
         ws = _scratch(nbytes, dev)
-        check(lib.ssd_conv1d_bwd(xp, ld, wp, bp, cu, gx, gb, gc, *po, io, n, nseq, cx, cb, width, bool(silu),
-                                 None if ws is None else ws.data_ptr(), nbytes, torch.cuda.current_stream(dev).cuda_stream))
+        check(f(xp, ld, wp, bp, cu, gx, gb, gc, *po, io, n, nseq, cx, cb, width, bool(silu),
+                None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev.index)))
     return out
 
 
 # --------------------------------------------------------------- selective scan
 
 def _sel_args(x, dt, A, B, C, D, z, dt_bias, softplus):
-    dev = _required(x=x, dt=dt, A=A, B=B, C=C)
+    dev = _device_of(x, "x")
+    _device_of(B, "B")
     _need_dim(x, "x", 2)
     _need_dim(B, "B", 3)
-    (n, d), (_, G, N), io = x.shape, B.shape, x.dtype
+    rows, io = x.shape, x.dtype
+    n, d = rows
+    _, G, N = B.shape
     a = _SelArgs()
     a.io_dtype = _io_of(x, "x")
-    a.x, a.x_stride = _rows(x, "x", io, dev, (n, d))
-    a.dt, a.dt_stride = _rows(dt, "dt", io, dev, (n, d))
-    a.z, a.z_stride = _rows(z, "z", io, dev, (n, d))
+    a.x, a.x_stride = _rows(x, "x", io, dev, rows)
+    a.dt, a.dt_stride = _rows(dt, "dt", io, dev, rows)
+    if z is not None:
+        a.z, a.z_stride = _rows(z, "z", io, dev, rows)
     a.B, a.b_stride = _rows(B, "B", io, dev, (n, G, N))
     a.C, a.c_stride = _rows(C, "C", io, dev, (n, G, N))
     a.A = _whole(A, "A", _f32, dev, (d, N))
-    a.D = _whole(D, "D", _f32, dev, (d,))
-    a.dt_bias = _whole(dt_bias, "dt_bias", _f32, dev, (d,))
+    a.D = _maybe(D, "D", _f32, dev, (d,))
+    a.dt_bias = _maybe(dt_bias, "dt_bias", _f32, dev, (d,))
     a.softplus, a.channels, a.ngroups, a.dstate = bool(softplus), d, G, N
     return a, dev, n, d, G, N
 
@@ -272,7 +285,7 @@ def _sel_args(x, dt, A, B, C, D, z, dt_bias, softplus):
 def _states(state, slots, rows, d, N, dev):
     _need_dim(state, "state", 3)
     nslots = state.shape[0]
-    return _whole(state, "state", _f32, dev, (nslots, d, N)), _whole(slots, "slots", torch.int32, dev, (rows,)), nslots
+    return _whole(state, "state", _f32, dev, (nslots, d, N)), _maybe(slots, "slots", torch.int32, dev, (rows,)), nslots
 
 
 def ssd_selective_scan_varlen(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, *, softplus=True, state=None,
@@ -285,23 +298,22 @@ def ssd_selective_scan_varlen(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bia
     float32 is read where has_init (bool [nseq]) says so and left holding each
     prompt's end state, in slot slots[i] (int32; None: i).  return_chunk_states keeps
     what ssd_selective_scan_bwd needs."""
-    lib, check = _lib_and_check()
+    f, check = _call("ssd_selective_scan_varlen")
     a, dev, n, d, _, N = _sel_args(x, dt, A, B, C, D, z, dt_bias, softplus)
     cu, nseq = _sequences(cu_seqlens, dev)
     sp = slp = None
     nslots = 0
     if state is not None:
         sp, slp, nslots = _states(state, slots, nseq, d, N, dev)
-    hip = _whole(has_init, "has_init", torch.bool, dev, (nseq,))
+    hip = _maybe(has_init, "has_init", torch.bool, dev, (nseq,))
     with _on(dev, stream):
         if y is None:
-            y = torch.empty((n, d), dtype=x.dtype, device=dev)
+            y = x.new_empty((n, d))
         kept = None
         if return_chunk_states:
-            kept = torch.empty((_size(lib.ssd_selective_scan_chunk_states(n, nseq), "the scan"), d, N), dtype=_f32, device=dev)
-        check(lib.ssd_selective_scan_varlen(a, cu, sp, slp, hip, None if kept is None else kept.data_ptr(),
-                                            _whole(y, "y", x.dtype, dev, (n, d)), n, nseq, nslots,
-                                            torch.cuda.current_stream(dev).cuda_stream))
+            kept = torch.empty((_size("ssd_selective_scan_chunk_states", n, nseq), d, N), dtype=_f32, device=dev)
+        check(f(a, cu, sp, slp, hip, None if kept is None else kept.data_ptr(), _whole(y, "y", x.dtype, dev, (n, d)), n,
+                nseq, nslots, _raw_stream(dev.index)))
     return y, kept
 
 
@@ -311,15 +323,14 @@ def ssd_selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=No
     float32 is updated in place.  x, dt, z [b, channels], B, C [b, G, N] (rows may be
     strided); sequence i uses slot slots[i] (None: i), and a negative slot skips it.
     Returns y [b, channels]."""
-    lib, check = _lib_and_check()
+    f, check = _call("ssd_selective_state_update")
     a, dev, n, d, _, N = _sel_args(x, dt, A, B, C, D, z, dt_bias, softplus)
-    _required(x=x, state=state)
+    _device_of(state, "state")
     sp, slp, nslots = _states(state, slots, n, d, N, dev)
     with _on(dev, stream):
         if y is None:
-            y = torch.empty((n, d), dtype=x.dtype, device=dev)
-        check(lib.ssd_selective_state_update(a, sp, slp, _whole(y, "y", x.dtype, dev, (n, d)), n, nslots,
-                                             torch.cuda.current_stream(dev).cuda_stream))
+            y = x.new_empty((n, d))
+        check(f(a, sp, slp, _whole(y, "y", x.dtype, dev, (n, d)), n, nslots, _raw_stream(dev.index)))
     return y
 
 
@@ -328,12 +339,11 @@ def ssd_selective_scan_bwd(x, dt, A, B, C, cu_seqlens, dy, chunk_states, D=None,
     """Gradients of ssd_selective_scan_varlen without states, from dy and the forward's
     chunk_states: dict of dx, ddt, dz, dB, dC (io dtype) and dA, dD, ddt_bias (float32);
     those of absent inputs are None.  ``out`` may pass them preallocated."""
-    lib, check = _lib_and_check()
+    f, check = _call("ssd_selective_scan_bwd")
     a, dev, n, d, G, N = _sel_args(x, dt, A, B, C, D, z, dt_bias, softplus)
     cu, nseq = _sequences(cu_seqlens, dev)
-    _required(dy=dy, chunk_states=chunk_states)
     gy = _whole(dy, "dy", x.dtype, dev, (n, d))
-    kept = _whole(chunk_states, "chunk_states", _f32, dev, (_size(lib.ssd_selective_scan_chunk_states(n, nseq), "the scan"), d, N))
+    kept = _whole(chunk_states, "chunk_states", _f32, dev, (_size("ssd_selective_scan_chunk_states", n, nseq), d, N))
     with _on(dev, stream):
         out = {} if out is None else out
         shapes = dict(dx=((n, d), x.dtype, x), ddt=((n, d), x.dtype, dt), dz=((n, d), x.dtype, z), dB=((n, G, N), x.dtype, B),
@@ -341,10 +351,9 @@ def ssd_selective_scan_bwd(x, dt, A, B, C, cu_seqlens, dy, chunk_states, D=None,
         po = [None if of is None else _fresh(out, k, s, t, dev) for k, (s, t, of) in shapes.items()]
         for k in shapes:
             out.setdefault(k, None)
-        nbytes = _size(lib.ssd_selective_scan_bwd_workspace_size(n, nseq, d, G, N), "the scan's gradient")
+        nbytes = _size("ssd_selective_scan_bwd_workspace_size", n, nseq, d, G, N)
         ws = _scratch(nbytes, dev)
-        check(lib.ssd_selective_scan_bwd(a, cu, gy, kept, *po, n, nseq, None if ws is None else ws.data_ptr(), nbytes,
-                                         torch.cuda.current_stream(dev).cuda_stream))
+        check(f(a, cu, gy, kept, *po, n, nseq, None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev.index)))
     return out
 
 
@@ -356,25 +365,25 @@ def ssd_residual_rmsnorm(x, weight, residual=None, scale=None, *, eps=1e-5, out=
     x [rows, width] bf16/float32, residual of x's dtype or float32 (rows of both may
     be strided), scale and weight [width] float32.  Returns (out, r): r in the
     residual's dtype (x's when there is none; residual_out may be residual itself)."""
-    lib, check = _lib_and_check()
-    dev = _required(x=x, weight=weight)
+    f, check = _call("ssd_residual_rmsnorm")
+    dev, t = _device_of(x, "x"), x.dtype
     _need_dim(x, "x", 2)
-    n, d = x.shape
-    rt = x.dtype if residual is None else residual.dtype
-    if rt not in (x.dtype, _f32):
-        raise ValueError("residual must have x's dtype or float32")
-    io = _io_of(x, "x")
-    xp, ldx = _rows(x, "x", x.dtype, dev, (n, d))
-    rp, ldr = _rows(residual, "residual", rt, dev, (n, d))
+    shape = n, d = x.shape
+    io, rt, rp, ldr = _io_of(x, "x"), t, None, 0
+    if residual is not None:
+        rt = residual.dtype
+        if rt != t and rt != _f32:
+            raise ValueError("residual must have x's dtype or float32")
+        rp, ldr = _rows(residual, "residual", rt, dev, shape)
+    xp, ldx = _rows(x, "x", t, dev, shape)
+    wp, sp = _whole(weight, "weight", _f32, dev, (d,)), _maybe(scale, "scale", _f32, dev, (d,))
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((n, d), dtype=x.dtype, device=dev)
+            out = x.new_empty(shape)
         if residual_out is None:
-            residual_out = torch.empty((n, d), dtype=rt, device=dev)
-        check(lib.ssd_residual_rmsnorm(xp, ldx, rp, ldr, _whole(scale, "scale", _f32, dev, (d,)),
-                                       _whole(weight, "weight", _f32, dev, (d,)), _whole(out, "out", x.dtype, dev, (n, d)),
-                                       _whole(residual_out, "residual_out", rt, dev, (n, d)), io, _IO[rt], n, d, eps,
-                                       torch.cuda.current_stream(dev).cuda_stream))
+            residual_out = x.new_empty(shape, dtype=rt)
+        check(f(xp, ldx, rp, ldr, sp, wp, _whole(out, "out", t, dev, shape), _whole(residual_out, "residual_out", rt, dev, shape),
+                io, _IO[rt], n, d, eps, _raw_stream(dev.index)))
     return out, residual_out
 
 
@@ -382,34 +391,44 @@ def ssd_residual_rmsnorm_bwd(residual, weight, dout, dresidual=None, x=None, sca
     """Gradients of ssd_residual_rmsnorm from the r it returned: dict of dresidual (r's
     dtype), dx (dout's dtype; the same tensor where neither scale nor a wider dtype
     sets them apart), dweight, and dscale (None without scale, which needs x)."""
-    lib, check = _lib_and_check()
-    dev = _required(residual=residual, weight=weight, dout=dout)
+    f, check = _call("ssd_residual_rmsnorm_bwd")
+    dev = _device_of(residual, "residual")
+    _device_of(dout, "dout")
     _need_dim(residual, "residual", 2)
-    (n, d), rt, t = residual.shape, residual.dtype, dout.dtype
+    shape, rt, t = residual.shape, residual.dtype, dout.dtype
+    n, d = shape
     io = _io_of(dout, "dout")
-    if rt not in (t, _f32):
+    if rt != t and rt != _f32:
         raise ValueError("residual must have dout's dtype or float32")
-    if scale is not None and x is None:
-        raise ValueError("x is required with scale")
-    rp, ldr = _rows(residual, "residual", rt, dev, (n, d))
-    xp, ldx = _rows(x, "x", t, dev, (n, d)) if scale is not None else (None, 0)
+    rp, ldr = _rows(residual, "residual", rt, dev, shape)
+    xp, ldx = _rows(x, "x", t, dev, shape) if scale is not None else (None, 0)
+    wp, sp = _whole(weight, "weight", _f32, dev, (d,)), _maybe(scale, "scale", _f32, dev, (d,))
+    up, ur = _whole(dout, "dout", t, dev, shape), _maybe(dresidual, "dresidual", rt, dev, shape)
     with _on(dev, stream):
         out = {} if out is None else out
-        gr, apart = _fresh(out, "dresidual", (n, d), rt, dev), scale is not None or rt != t
-        gx = _fresh(out, "dx", (n, d), t, dev) if apart else None
+        gr, apart = _fresh(out, "dresidual", shape, rt, dev), scale is not None or rt != t
+        gx = _fresh(out, "dx", shape, t, dev) if apart else None
         if not apart:
             out["dx"] = out["dresidual"]
         gw = _fresh(out, "dweight", (d,), _f32, dev)
         gs = None if scale is None else _fresh(out, "dscale", (d,), _f32, dev)
         out.setdefault("dscale", None)
-        nbytes = _size(lib.ssd_rmsnorm_bwd_workspace_size(n, d), "the norm's gradient")
+        nbytes = _size("ssd_rmsnorm_bwd_workspace_size", n, d)
         ws = _scratch(nbytes, dev)
-        check(lib.ssd_residual_rmsnorm_bwd(rp, ldr, _whole(weight, "weight", _f32, dev, (d,)), _whole(dout, "dout", t, dev, (n, d)),
-                                           _whole(dresidual, "dresidual", rt, dev, (n, d)), xp, ldx,
-                                           _whole(scale, "scale", _f32, dev, (d,)), gx, gr, gw, gs, io, _IO[rt], n, d, eps,
-                                           None if ws is None else ws.data_ptr(), nbytes,
-                                           torch.cuda.current_stream(dev).cuda_stream))
+        check(f(rp, ldr, wp, up, ur, xp, ldx, sp, gx, gr, gw, gs, io, _IO[rt], n, d, eps, None if ws is None else ws.data_ptr(),
+                nbytes, _raw_stream(dev.index)))
     return out
+
+
+def _gated_inputs(y, z, weight, scale):
+    dev, t = _device_of(y, "y"), y.dtype
+    _need_dim(y, "y", 2)
+    shape = y.shape
+    yp, ldy = _rows(y, "y", t, dev, shape)
+    zp, ldz = (None, 0) if z is None else _rows(z, "z", t, dev, shape)
+    width = (shape[1],)
+    return (dev, _io_of(y, "y"), shape, yp, ldy, zp, ldz, _whole(weight, "weight", _f32, dev, width),
+            _maybe(scale, "scale", _f32, dev, width))
 
 
 def ssd_gated_rmsnorm(y, z, weight, residual=None, scale=None, *, ngroups=1, norm_before_gate=False, eps=1e-5, out=None,
@@ -418,20 +437,14 @@ def ssd_gated_rmsnorm(y, z, weight, residual=None, scale=None, *, ngroups=1, nor
     rmsnorm(y) * weight * silu(z) with norm_before_gate; times scale and plus residual
     where they are given.  y, z (None: no gate), residual [rows, width] of one dtype
     (bf16/float32; rows may be strided), weight, scale [width] float32."""
-    lib, check = _lib_and_check()
-    dev = _required(y=y, weight=weight)
-    _need_dim(y, "y", 2)
-    n, d = y.shape
-    io = _io_of(y, "y")
-    yp, ldy = _rows(y, "y", y.dtype, dev, (n, d))
-    zp, ldz = _rows(z, "z", y.dtype, dev, (n, d))
-    rp, ldr = _rows(residual, "residual", y.dtype, dev, (n, d))
+    f, check = _call("ssd_gated_rmsnorm")
+    dev, io, shape, yp, ldy, zp, ldz, wp, sp = _gated_inputs(y, z, weight, scale)
+    rp, ldr = (None, 0) if residual is None else _rows(residual, "residual", y.dtype, dev, shape)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((n, d), dtype=y.dtype, device=dev)
-        check(lib.ssd_gated_rmsnorm(yp, ldy, zp, ldz, rp, ldr, _whole(scale, "scale", _f32, dev, (d,)),
-                                    _whole(weight, "weight", _f32, dev, (d,)), _whole(out, "out", y.dtype, dev, (n, d)), io, n, d,
-                                    ngroups, bool(norm_before_gate), eps, torch.cuda.current_stream(dev).cuda_stream))
+            out = y.new_empty(shape)
+        check(f(yp, ldy, zp, ldz, rp, ldr, sp, wp, _whole(out, "out", y.dtype, dev, shape), io, *shape, ngroups,
+                bool(norm_before_gate), eps, _raw_stream(dev.index)))
     return out
 
 
@@ -439,25 +452,19 @@ def ssd_gated_rmsnorm_bwd(y, z, weight, dout, scale=None, *, ngroups=1, norm_bef
                           stream=None):
     """Gradients of ssd_gated_rmsnorm: dict of dy, dz (None without z), dweight and
     dscale (None without scale); the residual's gradient is dout."""
-    lib, check = _lib_and_check()
-    dev = _required(y=y, weight=weight, dout=dout)
-    _need_dim(y, "y", 2)
-    n, d = y.shape
-    io = _io_of(y, "y")
-    yp, ldy = _rows(y, "y", y.dtype, dev, (n, d))
-    zp, ldz = _rows(z, "z", y.dtype, dev, (n, d))
+    f, check = _call("ssd_gated_rmsnorm_bwd")
+    dev, io, shape, yp, ldy, zp, ldz, wp, sp = _gated_inputs(y, z, weight, scale)
+    t, width = y.dtype, (shape[1],)
+    up = _whole(dout, "dout", t, dev, shape)
     with _on(dev, stream):
         out = {} if out is None else out
-        gy, gz = _fresh(out, "dy", (n, d), y.dtype, dev), None if z is None else _fresh(out, "dz", (n, d), y.dtype, dev)
-        gw = _fresh(out, "dweight", (d,), _f32, dev)
-        gs = None if scale is None else _fresh(out, "dscale", (d,), _f32, dev)
+        gy, gz = _fresh(out, "dy", shape, t, dev), None if z is None else _fresh(out, "dz", shape, t, dev)
+        gw = _fresh(out, "dweight", width, _f32, dev)
+        gs = None if scale is None else _fresh(out, "dscale", width, _f32, dev)
         out.setdefault("dz", None)
         out.setdefault("dscale", None)
-        nbytes = _size(lib.ssd_rmsnorm_bwd_workspace_size(n, d), "the norm's gradient")
+        nbytes = _size("ssd_rmsnorm_bwd_workspace_size", *shape)
         ws = _scratch(nbytes, dev)
-        check(lib.ssd_gated_rmsnorm_bwd(yp, ldy, zp, ldz, _whole(weight, "weight", _f32, dev, (d,)),
-                                        _whole(dout, "dout", y.dtype, dev, (n, d)), _whole(scale, "scale", _f32, dev, (d,)), gy, gz, gw, gs,
-                                        io, n, d, ngroups, bool(norm_before_gate), eps,
-                                        None if ws is None else ws.data_ptr(), nbytes,
-                                        torch.cuda.current_stream(dev).cuda_stream))
+        check(f(yp, ldy, zp, ldz, wp, up, sp, gy, gz, gw, gs, io, *shape, ngroups, bool(norm_before_gate), eps,
+                None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev.index)))
     return out

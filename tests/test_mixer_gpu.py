@@ -358,3 +358,24 @@ def test_scan_bwd(io, lens, d, G, N, pad, full):
             close(got[k], v, m, r + (n if k in ("dA", "dD", "ddt_bias") else d), k)
     again = ssd.ssd_selective_scan_bwd(*ins, cu, dy, kept, *opt, softplus=full)
     assert all(got[k] is None or torch.equal(got[k], again[k]) for k in got)
+
+
+@pytest.mark.parametrize("K", [2, 3, 4, 6, 8])
+@pytest.mark.parametrize("cx", [16, 5])
+def test_conv_sees_no_row_past_its_width(K, cx):
+    """An infinite input reaches the K rows of its own sequence that have it in their
+    window and no other, in both directions."""
+    g, n, bad = gen(K), 200, 100
+    for t0, cu in ((bad, bounds([n])), (bad, bounds([bad + 1, n - bad - 1])), (bad, bounds([bad - 1, n - bad + 1]))):
+        x, w, up = randn(g, n, cx), randn(g, cx, K), randn(g, n, cx)
+        x[t0] = float("inf")
+        lo, hi = next((a, b) for a, b in ref.spans(cu) if a <= t0 < b)
+        out = ssd.ssd_conv1d_varlen(x, w, None, cu, silu=False)[0]
+        touched = torch.zeros(n, dtype=torch.bool, device="cuda")
+        touched[t0:min(t0 + K, hi)] = True
+        assert torch.equal(~torch.isfinite(out).all(1), touched)
+        up[t0] = float("inf")
+        dx = ssd.ssd_conv1d_bwd(torch.zeros_like(x), w, None, cu, up, silu=False)["dxbc"]
+        touched[:] = False
+        touched[max(t0 - K + 1, lo):t0 + 1] = True
+        assert torch.equal(~torch.isfinite(dx).all(1), touched)
