@@ -200,7 +200,7 @@ struct SelCall {
     int softplus, channels, groups, dstate;
     Packed seq;
 };
-constexpr int SEL_CHUNK = 128;      // tokens between kept states
+constexpr int SEL_CHUNK = 128;  // tokens between kept states
 constexpr int SEL_MAX_DSTATE = 64;  // shared memory for B and C of a chunk
 cudaError_t launch_sel_varlen(const SelCall &c, cudaStream_t st);
 cudaError_t launch_sel_update(const SelCall &c, int batch, cudaStream_t st);

@@ -20,8 +20,48 @@
 namespace ssd {
 namespace {
 
-constexpr int TL = 8, K = 16, SEG = TL * K, CL = 32 / TL, CB = SEL_WARPS * CL;
-static_assert(SEG == SEL_CHUNK, "a chunk starts where its state was kept");
+constexpr int TL = 8, K = SEL_CHUNK / TL, SEG = SEL_CHUNK, CL = 32 / TL, CB = SEL_WARPS * CL;
+static_assert(CL == 4 && (K == 8 || K == 16), "the matrix instructions below sum 4 lanes, 8 or 16 tokens each");
+
+// Sums over the four channels of a warp by matrix instructions: D[token][lane run] +=
+// A[token][k] B[k][lane run], where B holds the lanes' values as they are (k: the four
+// lanes of a run, times two registers) and A is ones for the k of one token and zero
+// elsewhere.  One instruction sums two values of every lane over its run's channels,
+// where shuffles that halve the values took twelve (32 of the 43 instructions per state
+// and token were not the recurrence; the kernel took 1428 us against KERNEL_TIME at
+// 64 x 512 tokens of 1024 channels and 16 states).
+//   float32: each value goes in as two tf32 parts, its first 11 bits and the next 11, so
+//   that it keeps 2^-22; the sums are float32.
+//   bf16: the first part alone.  A product then loses what lies past 11 bits (below
+//   2^-10 of it, a quarter of a step of the bf16 gradient it goes into); the sums are
+//   float32 all the same.
+template <typename T> struct ChannelSum {
+    uint32_t one[8];  // row lane/4 of A has ones in its places for token i (mod 8)
+    __device__ __forceinline__ explicit ChannelSum(int lane) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) one[i] = (lane >> 2) == i ? 0x3f800000u : 0u;
+    }
+    static __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, float b0, float b1) {
+        asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+    }
+    // d[0], d[1]: token lane/4 (d[2], d[3]: + 8) of lane runs 2 (lane%4) and + 1
+    template <int H> __device__ __forceinline__ void operator()(const float2 (&v)[H], float (&d)[4]) const {
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const uint32_t p = one[(2 * i) & 7], q = one[(2 * i + 1) & 7];
+            const uint32_t a0 = i < 4 ? p : 0u, a1 = i < 4 ? 0u : p, a2 = i < 4 ? q : 0u, a3 = i < 4 ? 0u : q;
+            if constexpr (sizeof(T) == 4) {
+                const float x = __uint_as_float(__float_as_uint(v[i].x) & 0xffffe000u), y = __uint_as_float(__float_as_uint(v[i].y) & 0xffffe000u);
+                mma(d, a0, a1, a2, a3, x, y);
+                mma(d, a0, a1, a2, a3, v[i].x - x, v[i].y - y);
+            } else {
+                mma(d, a0, a1, a2, a3, v[i].x, v[i].y);
+            }
+        }
+    }
+};
 
 template <typename T> struct BwdShape {
     using Rows = RowTile<T, SEG, CB, TL>;
@@ -39,7 +79,7 @@ struct Parts {      // workspace
 
 // Where a lane stands and what its block holds in shared memory.
 struct Lane {
-    int l, cl, ch, w;    // lane run, channel of the warp, channel of the block, warp
+    int l, ch, w;        // lane run, channel of the block, warp
     int mine;            // real tokens of the run
     float bias, D;
     unsigned char *xs, *ds, *zs, *ys;
@@ -58,17 +98,16 @@ __device__ __forceinline__ void bwd_chunk(const SelCall &c, const Lane &a, float
     const int N = c.dstate, M = max(N, SEL_WARPS), l = a.l, ch = a.ch;
     float2 dl[H], u2[H], dp[H], du[H], sd[H], p2[H];
     float total = 0.f;
+    T *const px = Rows::row(a.xs, l * LEN, l) + ch, *const pd = Rows::row(a.ds, l * LEN, l) + ch;
+    T *const pz = Rows::row(a.zs, l * LEN, l) + ch, *const py = Rows::row(a.ys, l * LEN, l) + ch;
 #pragma unroll
     for (int k = 0; k < LEN; ++k) {
-        float d = 0.f, u = 0.f, e = 0.f;
-        if (k < a.mine) {
-            const int r = l * LEN + k;
-            d = ld_f32<T>(Rows::row(a.ds, r, l) + ch) + a.bias;
-            if (c.softplus) d = softplus_f(d);
-            u = d * ld_f32<T>(Rows::row(a.xs, r, l) + ch);
-            e = ld_f32<T>(Rows::row(a.ys, r, l) + ch);
-            if (c.z) e *= silu_v(ld_f32<T>(Rows::row(a.zs, r, l) + ch));
-        }
+        const bool in = k < a.mine;
+        float d = ld_f32<T>(pd + k * CB) + a.bias, e = ld_f32<T>(py + k * CB);
+        if (c.softplus) d = softplus_f(d);
+        if (c.z) e *= silu_v(ld_f32<T>(pz + k * CB));
+        d = in ? d : 0.f, e = in ? e : 0.f;
+        const float u = in ? d * ld_f32<T>(px + k * CB) : 0.f;
         total += d;
         if (k & 1)
             dl[k / 2].y = d, u2[k / 2].y = u, dp[k / 2].y = e;
@@ -77,29 +116,14 @@ __device__ __forceinline__ void bwd_chunk(const SelCall &c, const Lane &a, float
     }
 #pragma unroll
     for (int k = 0; k < H; ++k) du[k] = sd[k] = p2[k] = make_float2(0.f, 0.f);
-    // Sum of v over the warp's channels: lane cl ends with tokens 4 cl .. 4 cl + 3
-    // of its run, which it adds to the block's sums.
+    const ChannelSum<T> channel_sum(threadIdx.x & 31);
+    // The sum of v over the warp's channels into the block's sums, [token][lane run].
     auto reduce = [&](const float2 (&v)[H], float *acc) {
-        float v8[8], sum[4];
-        const float2 none = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {  // cl bit 1: the run's halves
-            const float2 first = k < H ? v[k < H ? k : 0] : none, second = k + 4 < H ? v[k + 4 < H ? k + 4 : 0] : none;
-            const float2 keep = a.cl & 2 ? second : first, give = a.cl & 2 ? first : second;
-            v8[2 * k] = keep.x + __shfl_xor_sync(0xffffffffu, give.x, 2 * TL);
-            v8[2 * k + 1] = keep.y + __shfl_xor_sync(0xffffffffu, give.y, 2 * TL);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {  // cl bit 0: quads
-            const float keep = a.cl & 1 ? v8[k + 4] : v8[k], give = a.cl & 1 ? v8[k] : v8[k + 4];
-            sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, TL);
-        }
-        if (a.cl < Q) {
-            float4 *o = reinterpret_cast<float4 *>(acc + (a.cl * TL + l) * 4);
-            float4 t = *o;
-            t.x += sum[0], t.y += sum[1], t.z += sum[2], t.w += sum[3];
-            *o = t;
-        }
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        channel_sum(v, d);
+        float2 *o = reinterpret_cast<float2 *>(acc) + (threadIdx.x & 31);
+        *o = add2(*o, make_float2(d[0], d[1]));
+        if (LEN > 8) o[32] = add2(o[32], make_float2(d[2], d[3]));
     };
 #pragma unroll 1
     for (int it = 0; it < M; ++it) {
@@ -126,10 +150,10 @@ __device__ __forceinline__ void bwd_chunk(const SelCall &c, const Lane &a, float
             if (l == 0) S_ = fmaf(P, hc, S_);
 #pragma unroll
             for (int o = 1; o < TL; o *= 2) {
-                const float Sp = __shfl_up_sync(0xffffffffu, S_, o, TL), Pp = __shfl_up_sync(0xffffffffu, P, o, TL);
+                const float Sp = __shfl_up_sync(0xffffffffu, S_, o * CL), Pp = __shfl_up_sync(0xffffffffu, P, o * CL);
                 if (l >= o) S_ = fmaf(P, Sp, S_), P *= Pp;
             }
-            float h = __shfl_up_sync(0xffffffffu, S_, 1, TL);
+            float h = __shfl_up_sync(0xffffffffu, S_, CL);
             if (l == 0) h = hc;
 #pragma unroll
             for (int k = 0; k < H; ++k) {
@@ -154,10 +178,10 @@ __device__ __forceinline__ void bwd_chunk(const SelCall &c, const Lane &a, float
             if (l == TL - 1) R = fmaf(P, gc, R);
 #pragma unroll
             for (int o = 1; o < TL; o *= 2) {
-                const float Rn = __shfl_down_sync(0xffffffffu, R, o, TL), Pn = __shfl_down_sync(0xffffffffu, P, o, TL);
+                const float Rn = __shfl_down_sync(0xffffffffu, R, o * CL), Pn = __shfl_down_sync(0xffffffffu, P, o * CL);
                 if (l + o < TL) R = fmaf(P, Rn, R), P *= Pn;
             }
-            float G = __shfl_down_sync(0xffffffffu, R, 1, TL);
+            float G = __shfl_down_sync(0xffffffffu, R, CL);
             if (l == TL - 1) G = gc;
             if (l == 0) a.gs[s * CB + ch] = R;
             float2 dA2 = make_float2(0.f, 0.f);
@@ -175,32 +199,31 @@ __device__ __forceinline__ void bwd_chunk(const SelCall &c, const Lane &a, float
             reduce(v2, a.sB + s * SEG);
             float dA = dA2.x + dA2.y;
 #pragma unroll
-            for (int o = 1; o < TL; o *= 2) dA += __shfl_xor_sync(0xffffffffu, dA, o);
+            for (int o = CL; o < 32; o *= 2) dA += __shfl_xor_sync(0xffffffffu, dA, o);
             if (l == 0) a.dAs[s * CB + ch] += dA;
         }
         __syncthreads();  // the next state's sums
     }
 #pragma unroll
     for (int k = 0; k < LEN; ++k) {
-        if (k < a.mine) {
-            const int r = l * LEN + k;
-            const float d = k & 1 ? dl[k / 2].y : dl[k / 2].x, e = k & 1 ? dp[k / 2].y : dp[k / 2].x;
-            const float duk = k & 1 ? du[k / 2].y : du[k / 2].x;
-            const float sdk = (k & 1 ? sd[k / 2].y : sd[k / 2].x) * 0.6931471805599453f;  // A was scaled by log2 e
-            T *px = Rows::row(a.xs, r, l) + ch, *pd = Rows::row(a.ds, r, l) + ch;
-            const float xv = ld_f32<T>(px);
-            float ddt = fmaf(xv, duk, sdk);
-            if (c.softplus) ddt *= sigmoid_f(ld_f32<T>(pd) + a.bias);
-            st_f32<T>(px, fmaf(d, duk, a.D * e));
-            st_f32<T>(pd, ddt);
-            dD = fmaf(e, xv, dD);
-            dbias += ddt;
-            if (c.z) {
-                T *pz = Rows::row(a.zs, r, l) + ch;
-                const float zv = ld_f32<T>(pz), sg = sigmoid_f(zv);
-                const float pre = fmaf(a.D, xv, k & 1 ? p2[k / 2].y : p2[k / 2].x);
-                st_f32<T>(pz, ld_f32<T>(Rows::row(a.ys, r, l) + ch) * pre * sg * fmaf(zv, 1.f - sg, 1.f));
-            }
+        const bool in = k < a.mine;
+        const float d = k & 1 ? dl[k / 2].y : dl[k / 2].x, e = k & 1 ? dp[k / 2].y : dp[k / 2].x;
+        const float duk = k & 1 ? du[k / 2].y : du[k / 2].x;
+        const float sdk = (k & 1 ? sd[k / 2].y : sd[k / 2].x) * 0.6931471805599453f;  // A was scaled by log2 e
+        const float xv = ld_f32<T>(px + k * CB);
+        float ddt = fmaf(xv, duk, sdk);
+        if (c.softplus) ddt *= sigmoid_f(ld_f32<T>(pd + k * CB) + a.bias);
+        dD += in ? e * xv : 0.f;
+        dbias += in ? ddt : 0.f;
+        if (c.z) {
+            const float zv = ld_f32<T>(pz + k * CB), sg = sigmoid_f(zv);
+            const float pre = fmaf(a.D, xv, k & 1 ? p2[k / 2].y : p2[k / 2].x);
+            const float dz = ld_f32<T>(py + k * CB) * pre * sg * fmaf(zv, 1.f - sg, 1.f);
+            if (in) st_f32<T>(pz + k * CB, dz);
+        }
+        if (in) {
+            st_f32<T>(px + k * CB, fmaf(d, duk, a.D * e));
+            st_f32<T>(pd + k * CB, ddt);
         }
     }
 }
@@ -223,7 +246,7 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, 1) sel_bwd_kernel(SelCall c, P
     const int cols = min(CB, (g + 1) * per_group - c0);
     int lo, hi;
     if (!seq_rows(c.seq, i, lo, hi)) lo = hi = 0;
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, l = lane % TL, cl = lane / TL, ch = w * CL + cl;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, l = lane / CL, ch = w * CL + lane % CL;
     const int chc = min(ch, cols - 1);
     const float bias = c.dt_bias ? c.dt_bias[c0 + chc] : 0.f, Dv = c.D ? c.D[c0 + chc] : 0.f;
     const T *x = static_cast<const T *>(c.x) + c0, *dt = static_cast<const T *>(c.dt) + c0,
@@ -235,10 +258,10 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, 1) sel_bwd_kernel(SelCall c, P
         gs[n * CB + cc] = dAs[n * CB + cc] = 0.f;
     }
     float dD = 0.f, dbias = 0.f;
-    Lane at{l, cl, ch, w, 0, bias, Dv, xs, ds, zs, ys, bc, As, hs, gs, dAs, sB, sC};
+    Lane at{l, ch, w, 0, bias, Dv, xs, ds, zs, ys, bc, As, hs, gs, dAs, sB, sC};
     const int chunks = (hi - lo + SEG - 1) / SEG;
     for (int chunk = chunks - 1; chunk >= 0; --chunk) {
-        const int t0 = lo + chunk * SEG, n = min(SEG, hi - t0), len = ((n + TL - 1) / TL + 3) & ~3;
+        const int t0 = lo + chunk * SEG, n = min(SEG, hi - t0), per_lane = (n + TL - 1) / TL, len = per_lane <= 4 ? 4 : per_lane <= 8 ? 8 : K;
         __syncthreads();  // the tiles are free again
         Rows::fetch(xs, x + t0 * c.ld_x, c.ld_x, n, cols, len, wide);
         Rows::fetch(ds, dt + t0 * c.ld_dt, c.ld_dt, n, cols, len, wide);
@@ -253,12 +276,12 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, 1) sel_bwd_kernel(SelCall c, P
         cp_wait<0>();
         __syncthreads();
         at.mine = ch < cols ? max(0, min(len, n - l * len)) : 0;
-        switch (len / 4) {
-        case 1: bwd_chunk<T, 1>(c, at, dD, dbias); break;
-        case 2: bwd_chunk<T, 2>(c, at, dD, dbias); break;
-        case 3: bwd_chunk<T, 3>(c, at, dD, dbias); break;
-        default: bwd_chunk<T, 4>(c, at, dD, dbias); break;
-        }
+        if (len == 4)
+            bwd_chunk<T, 1>(c, at, dD, dbias);
+        else if (K == 8 || len == 8)
+            bwd_chunk<T, 2>(c, at, dD, dbias);
+        else if (K == 16)
+            bwd_chunk<T, K / 4>(c, at, dD, dbias);
         __syncthreads();
         const size_t row0 = (size_t)t0 * c.channels + c0;
         Rows::flush(xs, static_cast<T *>(c.dx) + row0, c.channels, n, cols, len, wide);
@@ -266,7 +289,7 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, 1) sel_bwd_kernel(SelCall c, P
         if (c.z) Rows::flush(zs, static_cast<T *>(c.dz) + row0, c.channels, n, cols, len, wide);
         float *pb = parts.bc + ((size_t)blockIdx.y * c.seq.tokens + t0) * 2 * N;
         for (int u = threadIdx.x; u < n * N; u += SEL_WARPS * 32) {
-            const int r = u / N, s = u - r * N, o = s * SEG + BC::at(r, len);
+            const int r = u / N, s = u - r * N, run = r / len, o = s * SEG + (r - run * len) * TL + run;
             pb[r * 2 * N + s] = sB[o];
             pb[r * 2 * N + N + s] = sC[o];
         }
@@ -275,7 +298,7 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, 1) sel_bwd_kernel(SelCall c, P
     float *pa = parts.a + ((size_t)i * c.channels + c0) * N;
     for (int u = threadIdx.x; u < cols * N; u += SEL_WARPS * 32) pa[u] = dAs[(u % N) * CB + u / N];
 #pragma unroll
-    for (int o = 1; o < TL; o *= 2) {
+    for (int o = CL; o < 32; o *= 2) {
         dD += __shfl_xor_sync(0xffffffffu, dD, o);
         dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
     }

@@ -2,8 +2,8 @@
 // split of a chunk over a warp, and the staging of its rows in shared memory.
 //
 // A warp holds 32 / TL channels; the TL lanes of a channel hold consecutive runs
-// of `len` <= K tokens each (len a multiple of 4, chosen per chunk so that short
-// sequences waste little).  Token r of a chunk is item r % len of lane r / len.
+// of `len` = 4, 8 or 16 tokens each (chosen per chunk so that short sequences waste
+// little).  Token r of a chunk is item r % len of lane r / len.
 // Within its run a lane walks the recurrence in registers; runs are joined by a
 // scan over the lanes of (decay, state) pairs.  One exponential per state and
 // token is all the recurrence needs, whatever the split.
@@ -34,32 +34,34 @@ template <typename T, int SEG, int CB, int TL> struct RowTile {
     // every row start is 16-byte aligned and cols * sizeof(T) a multiple of 16.
     static __device__ __forceinline__ void fetch(unsigned char *base, const T *src, long long ld, int n, int cols, int len,
                                                  bool wide) {
+        const int sh = 31 - __clz(len);
         if (wide) {
             constexpr int E = 16 / (int)sizeof(T), PER = CB / E;
             for (int u = threadIdx.x; u < n * PER; u += SEL_WARPS * 32) {
                 const int r = u / PER, k = (u % PER) * E;
-                if (k < cols) cp16(row(base, r, r / len) + k, src + r * ld + k);
+                if (k < cols) cp16(row(base, r, r >> sh) + k, src + r * ld + k);
             }
         } else {
             for (int u = threadIdx.x; u < n * CB; u += SEL_WARPS * 32) {
                 const int r = u / CB, k = u % CB;
-                if (k < cols) row(base, r, r / len)[k] = src[r * ld + k];
+                if (k < cols) row(base, r, r >> sh)[k] = src[r * ld + k];
             }
         }
     }
     // The reverse, for results.
     static __device__ __forceinline__ void flush(unsigned char *base, T *dst, long long ld, int n, int cols, int len, bool wide) {
+        const int sh = 31 - __clz(len);
         if (wide) {
             constexpr int E = 16 / (int)sizeof(T), PER = CB / E;
             for (int u = threadIdx.x; u < n * PER; u += SEL_WARPS * 32) {
                 const int r = u / PER, k = (u % PER) * E;
                 if (k < cols)
-                    *reinterpret_cast<uint4 *>(dst + r * ld + k) = *reinterpret_cast<const uint4 *>(row(base, r, r / len) + k);
+                    *reinterpret_cast<uint4 *>(dst + r * ld + k) = *reinterpret_cast<const uint4 *>(row(base, r, r >> sh) + k);
             }
         } else {
             for (int u = threadIdx.x; u < n * CB; u += SEL_WARPS * 32) {
                 const int r = u / CB, k = u % CB;
-                if (k < cols) dst[r * ld + k] = row(base, r, r / len)[k];
+                if (k < cols) dst[r * ld + k] = row(base, r, r >> sh)[k];
             }
         }
     }
@@ -72,7 +74,7 @@ template <typename T, int SEG, int TL> struct BCTile {
     static constexpr bool PACK = sizeof(T) == 2;
     static constexpr int STATE_WORDS = PACK ? SEG : 2 * SEG;
     static __device__ __forceinline__ int at(int r, int len) {
-        const int l = r / len, i = r - l * len;
+        const int l = r >> (31 - __clz(len)), i = r - l * len;
         return ((i >> 2) * TL + l) * 4 + (i & 3);
     }
     static __device__ __forceinline__ void put(uint32_t *bc, int s, int o, float b, float c) {

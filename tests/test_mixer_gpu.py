@@ -355,7 +355,10 @@ def test_scan_bwd(io, lens, d, G, N, pad, full):
         if not full and k in ("dD", "dz", "ddt_bias"):
             assert got[k] is None
         else:
-            close(got[k], v, m, r + (n if k in ("dA", "dD", "ddt_bias") else d), k)
+            # dB and dC in bf16: each product enters its sum without its bits past tf32's
+            # eleven, less than 2^-10 = 2^14 2^-24 of it, so the sum is off by less than 2^-10 M
+            short = 2 ** 14 if io == torch.bfloat16 and k in ("dB", "dC") else 0
+            close(got[k], v, m, r + (n if k in ("dA", "dD", "ddt_bias") else d) + short, k)
     again = ssd.ssd_selective_scan_bwd(*ins, cu, dy, kept, *opt, softplus=full)
     assert all(got[k] is None or torch.equal(got[k], again[k]) for k in got)
 
