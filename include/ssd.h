@@ -468,18 +468,21 @@ typedef struct {
 } ssd_sel_args;
 
 /*
- * The scan on packed sequences, one launch, no workspace.
+ * The scan on packed sequences: one launch, or three and a workspace where sequences
+ * are cut into segments to fill the GPU (few sequences and channels; the state at a
+ * cut is carried over exactly like the states of ssd_fold_states).
  *  state  [nslots, channels, dstate] float32, or NULL: every sequence from zero
- *  chunk_states  NULL, or [ssd_selective_scan_chunk_states(tokens, nseq), channels,
- *         dstate] float32: the states before every 128th token of each sequence,
+ *  chunk_states  NULL, or [ssd_selective_scan_chunk_states(tokens, nseq), dstate,
+ *         channels] float32: the states before every 16th token of each sequence,
  *         which ssd_selective_scan_bwd reads (entries of no sequence stay unwritten)
  *  y      [tokens, channels] io_dtype, contiguous
  */
 size_t ssd_selective_scan_chunk_states(int tokens, int nseq);
+size_t ssd_selective_scan_workspace_size(int tokens, int nseq, int channels, int dstate);
 ssd_status ssd_selective_scan_varlen(const ssd_sel_args *args, const int *cu_seqlens, float *state,
                                      const int *slots, const unsigned char *has_init,
                                      float *chunk_states, void *y, int tokens, int nseq, int nslots,
-                                     void *stream);
+                                     void *workspace, size_t workspace_bytes, void *stream);
 
 /* One token per sequence, state [nslots, channels, dstate] float32 in place,
  * y [batch, channels].  batch <= 65535. */
@@ -492,7 +495,7 @@ ssd_status ssd_selective_state_update(const ssd_sel_args *args, float *state, co
  * is) [tokens, channels] and dB, dC [tokens, ngroups, dstate] in io_dtype,
  * contiguous, and dA [channels, dstate], dD and ddt_bias [channels] (or NULL)
  * float32.  Sums run in a fixed order.  The states inside a chunk are formed
- * again.  Two launches and a workspace.
+ * again.  Two launches (four where sequences are cut) and a workspace.
  */
 size_t ssd_selective_scan_bwd_workspace_size(int tokens, int nseq, int channels, int ngroups, int dstate);
 ssd_status ssd_selective_scan_bwd(const ssd_sel_args *args, const int *cu_seqlens, const void *dy,

@@ -191,7 +191,7 @@ struct SelCall {
     long long ld_x, ld_dt, ld_z, ld_b, ld_c;        // row strides
     const float *A, *D, *dt_bias;                   // [channels, dstate], [channels] or NULL
     float *state;                                   // [nslots, channels, dstate] or NULL
-    float *chunk_states;                            // [tokens/128 + nseq, channels, dstate] or NULL
+    float *chunk_states;                            // [tokens / SEL_CHUNK + nseq, dstate, channels] or NULL
     void *y;                                        // [tokens, channels]
     const void *dy;                                 // backward
     void *dx, *ddt, *dz, *dB, *dC;
@@ -200,9 +200,10 @@ struct SelCall {
     int softplus, channels, groups, dstate;
     Packed seq;
 };
-constexpr int SEL_CHUNK = 128;  // tokens between kept states
-constexpr int SEL_MAX_DSTATE = 64;  // shared memory for B and C of a chunk
-cudaError_t launch_sel_varlen(const SelCall &c, cudaStream_t st);
+constexpr int SEL_CHUNK = 16;  // tokens between kept states
+constexpr int SEL_MAX_DSTATE = 64;  // states of a channel in registers
+size_t sel_fwd_workspace(int tokens, int nseq, int channels, int dstate);
+cudaError_t launch_sel_varlen(const SelCall &c, float *ws, cudaStream_t st);
 cudaError_t launch_sel_update(const SelCall &c, int batch, cudaStream_t st);
 size_t sel_bwd_workspace(int tokens, int nseq, int channels, int groups, int dstate);
 cudaError_t launch_sel_bwd(const SelCall &c, void *ws, cudaStream_t st);

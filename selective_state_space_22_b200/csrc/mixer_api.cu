@@ -245,9 +245,15 @@ size_t ssd_selective_scan_chunk_states(int tokens, int nseq) {
     return (size_t)(tokens / ssd::SEL_CHUNK) + nseq;
 }
 
+size_t ssd_selective_scan_workspace_size(int tokens, int nseq, int channels, int dstate) {
+    if (tokens < 0 || nseq < 0 || tokens > kMaxRows || nseq > kMaxRows || check_sel(SSD_F32, channels, 1, dstate) != SSD_OK)
+        return SSD_WORKSPACE_INVALID;
+    return ssd::sel_fwd_workspace(tokens, nseq, channels, dstate);
+}
+
 ssd_status ssd_selective_scan_varlen(const ssd_sel_args *args, const int *cu_seqlens, float *state, const int *slots,
                                      const unsigned char *has_init, float *chunk_states, void *y, int tokens, int nseq,
-                                     int nslots, void *stream) {
+                                     int nslots, void *workspace, size_t workspace_bytes, void *stream) {
     ssd_status s = check_packed(tokens, nseq, cu_seqlens);
     if (s == SSD_OK) s = check_slots(state, slots, nslots, nseq);
     if (s != SSD_OK || tokens == 0 || nseq == 0) return s;
@@ -257,11 +263,15 @@ ssd_status ssd_selective_scan_varlen(const ssd_sel_args *args, const int *cu_seq
     NEED(y);
     NEED_16(y);
     NEED_16(chunk_states);
+    const size_t need = ssd::sel_fwd_workspace(tokens, nseq, c.channels, c.dstate);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return refuse(SSD_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need, workspace ? workspace_bytes : (size_t)0);
+    NEED_16(workspace);
     int *err = ssd::device_error_word();
     if (!err) return SSD_ERR_CUDA;
     c.state = state, c.chunk_states = chunk_states, c.y = y;
     c.seq = ssd::Packed{cu_seqlens, nseq, tokens, slots, nslots, has_init, err};
-    return done(ssd::launch_sel_varlen(c, static_cast<cudaStream_t>(stream)), "selective_scan_varlen launch");
+    return done(ssd::launch_sel_varlen(c, static_cast<float *>(workspace), static_cast<cudaStream_t>(stream)), "selective_scan_varlen launch");
 }
 
 ssd_status ssd_selective_state_update(const ssd_sel_args *args, float *state, const int *slots, void *y, int batch,

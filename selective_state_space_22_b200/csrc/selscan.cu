@@ -4,160 +4,155 @@
 //   h_t[n] = exp(delta_t A[n]) h_{t-1}[n] + delta_t x_t B_t[n],
 //   y_t = (sum_n C_t[n] h_t[n] + D x_t) silu(z_t)          per channel.
 //
-// A block takes one sequence and SEL_WARPS * 32 / TL channels of one B/C group and
-// walks the sequence in chunks; inside a chunk the tokens of a channel are split
-// over TL lanes (selscan_tile.cuh).  The split over time inside the warp keeps the
-// exponentials at one per state and token, where a second pass over chunks would
-// double them, and gives a single prompt enough warps.  Bound by the exponential
-// unit (N per channel and token at 16 per SM and clock) and by issue, then HBM.
-#include "selscan_tile.cuh"
+// A thread per channel, its states in registers, along a sequence or a segment of one
+// (selscan_seg.cuh): three packed operations and an exponential per state and token,
+// some forty more per token.  x, dt, z and y go straight between global memory and
+// registers (neighbouring lanes, neighbouring channels), four tokens ahead; B and C,
+// which a block's channels share, through shared memory.  Bound by the exponential
+// unit (N + 4 operations per channel and token at 16 per SM and clock), then by issue.
+// A first form split the tokens of a chunk over the lanes of a warp, with one
+// exponential per state and token at any length; its scans over lanes and the second
+// walk they need left it at 352 us where this one takes KERNEL_TIME (64 x 512 tokens,
+// 1024 channels, 16 states).
+#include "selscan_seg.cuh"
 
 namespace ssd {
 namespace {
 
-template <typename T, int TL, int K> struct FwdShape {
-    static constexpr int SEG = TL * K, CL = 32 / TL, CB = SEL_WARPS * CL;
-    using Rows = RowTile<T, SEG, CB, TL>;
-    using BC = BCTile<T, SEG, TL>;
-    static size_t smem(int N) { return 3 * (size_t)Rows::BYTES + (size_t)N * BC::STATE_WORDS * 4 + 2 * (size_t)CB * N * 4; }
-};
+constexpr int FWD_THREADS = 64, AHEAD = 4;
 
-// One chunk: the lane's tokens (4 Q slots, `mine` of them real) of channel ch, over
-// all states.  Q is a compile-time number so that the arrays stay in registers and
-// the state loop has no branches.
-template <typename T, int TL, int K, int Q>
-__device__ __forceinline__ void fwd_chunk(const SelCall &c, unsigned char *xs, unsigned char *ds, unsigned char *zs,
-                                          const uint32_t *bc, const float *As, float *hs, int l, int ch, int mine, float bias,
-                                          float Dv) {
-    using S = FwdShape<T, TL, K>;
-    using Rows = typename S::Rows;
-    using BC = typename S::BC;
-    constexpr int CB = S::CB, LEN = 4 * Q;
-    const int N = c.dstate;
-    float2 dl[LEN / 2], u2[LEN / 2], y2[LEN / 2];
-    float total = 0.f;
-    T *const px = Rows::row(xs, l * LEN, l) + ch;
-    const T *const pd = Rows::row(ds, l * LEN, l) + ch, *const pz = Rows::row(zs, l * LEN, l) + ch;
+// FULL: y, kept states and the end state; else only what sel_join needs.
+template <typename T, int NP, bool FULL>
+__global__ void __launch_bounds__(FWD_THREADS) sel_fwd_kernel(SelCall c, Segments sg, bool wide) {
+    constexpr int P = NP / 2, TT = NP <= 16 ? 32 : 16;
+    using Stage = StageBC<T, NP, TT, FWD_THREADS>;
+    __shared__ __align__(16) float4 bc[2][Stage::BYTES / 16];
+    int i, first, lo, hi, end;
+    if (!segment(c.seq, sg.seg, blockIdx.x, i, first, lo, hi, end)) return;  // the same for the whole block
+    if (!FULL && hi == end) return;  // nothing follows
+    const Mine me = my_channel<FWD_THREADS>(c, blockIdx.y);
+    const int N = c.dstate, d = me.channel, slot = FULL && c.state ? slot_of(c.seq.slots, c.seq.nslots, i, c.seq.dev_error) : -1;
+    const T *B = static_cast<const T *>(c.B) + me.group * N + lo * c.ld_b, *C = static_cast<const T *>(c.C) + me.group * N + lo * c.ld_c;
+    Stage stage;
+    stage.load(B, c.ld_b, C, c.ld_c, min(TT, hi - lo), N, wide);
+    float2 A2[P], h[P];
+    float *const state = c.state + (slot >= 0 ? ((size_t)slot * c.channels + d) * N : 0);
+    const bool init = slot >= 0 && c.seq.has_init && c.seq.has_init[i] && sg.seg == WHOLE;
+    float *const carried = sg.state + ((size_t)blockIdx.x * N) * c.channels + d;
+    auto load_h = [&](int n) {
+        if (n >= N) return 0.f;
+        if (FULL && sg.seg != WHOLE) return carried[(size_t)n * c.channels];
+        return init ? state[n] : 0.f;
+    };
 #pragma unroll
-    for (int k = 0; k < LEN; ++k) {
-        const bool in = k < mine;
-        float d = ld_f32<T>(pd + k * CB) + bias;
-        if (c.softplus) d = softplus_f(d);
-        d = in ? d : 0.f;
-        const float u = in ? d * ld_f32<T>(px + k * CB) : 0.f;
-        total += d;
-        if (k & 1)
-            dl[k / 2].y = d, u2[k / 2].y = u;
-        else
-            dl[k / 2].x = d, u2[k / 2].x = u;
+    for (int p = 0; p < P; ++p) {
+        A2[p] = make_float2(2 * p < N ? c.A[(size_t)d * N + 2 * p] * LOG2E : 0.f, 2 * p + 1 < N ? c.A[(size_t)d * N + 2 * p + 1] * LOG2E : 0.f);
+        h[p] = make_float2(load_h(2 * p), load_h(2 * p + 1));
     }
+    const float bias = c.dt_bias ? c.dt_bias[d] : 0.f, Dv = c.D ? c.D[d] : 0.f;
+    const T *px = static_cast<const T *>(c.x) + lo * c.ld_x + d, *pd = static_cast<const T *>(c.dt) + lo * c.ld_dt + d;
+    const T *pz = static_cast<const T *>(c.z) + (c.z ? lo * c.ld_z + d : 0);
+    T *py = static_cast<T *>(c.y) + (size_t)lo * c.channels + d;
+    T nx[AHEAD], nd[AHEAD], nz[AHEAD];
+    int left = hi - lo;  // tokens not yet fetched
+    auto fetch = [&] {
 #pragma unroll
-    for (int k = 0; k < LEN / 2; ++k) y2[k] = make_float2(0.f, 0.f);
-#pragma unroll 1
-    for (int s = 0; s < N; ++s) {
-        const float A2 = As[s * CB + ch], hc = hs[s * CB + ch];
-        const float2 A22 = splat(A2);
-        float2 a2[LEN / 2], b2[LEN / 2], c2[LEN / 2];
-        float S_ = 0.f, P = ex2a(A2 * total);
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            BC::quad(bc, s, q, l, b2 + 2 * q, c2 + 2 * q);
-#pragma unroll
-            for (int k = 2 * q; k < 2 * q + 2; ++k) {
-                const float2 arg = mul2(dl[k], A22);
-                a2[k] = make_float2(ex2a(arg.x), ex2a(arg.y));
-                b2[k] = mul2(u2[k], b2[k]);
-                S_ = fmaf(a2[k].x, S_, b2[k].x);
-                S_ = fmaf(a2[k].y, S_, b2[k].y);
+        for (int k = 0; k < AHEAD; ++k) {
+            if (k < left) {
+                nx[k] = *px, nd[k] = *pd;
+                if (FULL && c.z) nz[k] = *pz, pz += c.ld_z;
+                px += c.ld_x, pd += c.ld_dt;
             }
         }
-        if (l == 0) S_ = fmaf(P, hc, S_);
+        left -= AHEAD;
+    };
+    fetch();
+    stage.put(bc[0]);
+    float steps = 0.f;
+    float *kept = nullptr;
+    if (FULL && c.chunk_states) kept = c.chunk_states + ((size_t)(first / SEL_CHUNK + i + (lo - first) / SEL_CHUNK) * N) * c.channels + d;
+    for (int t0 = lo, buf = 0; t0 < hi; t0 += TT, buf ^= 1) {
+        const int nt = min(TT, hi - t0);
+        B += TT * c.ld_b, C += TT * c.ld_c;
+        if (t0 + TT < hi) stage.load(B, c.ld_b, C, c.ld_c, min(TT, hi - t0 - TT), N, wide);
+        __syncthreads();  // bc[buf] is written, and nobody reads bc[buf ^ 1] any more
+#pragma unroll 1
+        for (int t = 0; t < nt; t += AHEAD) {
+            float dl[AHEAD], xv[AHEAD], gate[AHEAD];
 #pragma unroll
-        for (int o = 1; o < TL; o *= 2) {
-            const float Sp = __shfl_up_sync(0xffffffffu, S_, o, TL), Pp = __shfl_up_sync(0xffffffffu, P, o, TL);
-            if (l >= o) S_ = fmaf(P, Sp, S_), P *= Pp;
-        }
-        float h = __shfl_up_sync(0xffffffffu, S_, 1, TL);
-        if (l == 0) h = hc;
-        if (l == TL - 1) hs[s * CB + ch] = S_;
+            for (int k = 0; k < AHEAD; ++k) {
+                xv[k] = ld_f32<T>(&nx[k]);
+                dl[k] = ld_f32<T>(&nd[k]) + bias;
+                if (c.softplus) dl[k] = softplus_f(dl[k]);
+                if (FULL) gate[k] = c.z ? silu_v(ld_f32<T>(&nz[k])) : 1.f;
+            }
+            fetch();
+            if (FULL && kept && (t0 - first + t) % SEL_CHUNK == 0) {
+                if (me.in)
 #pragma unroll
-        for (int k = 0; k < LEN / 2; ++k) {
-            float2 hh;
-            hh.x = h = fmaf(a2[k].x, h, b2[k].x);
-            hh.y = h = fmaf(a2[k].y, h, b2[k].y);
-            y2[k] = fma2(c2[k], hh, y2[k]);
+                    for (int n = 0; n < NP; ++n)
+                        if (n < N) kept[(size_t)n * c.channels] = n & 1 ? h[n / 2].y : h[n / 2].x;
+                kept += (size_t)N * c.channels;
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                if (t + k >= nt) break;
+                const float2 d2 = splat(dl[k]), u2 = splat(dl[k] * xv[k]);
+                float2 y2 = make_float2(0.f, 0.f);
+                const float4 *q = bc[buf] + (t + k) * P;
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const float4 v = q[p];
+                    const float2 arg = mul2(d2, A2[p]);
+                    h[p] = fma2(make_float2(ex2a(arg.x), ex2a(arg.y)), h[p], mul2(u2, make_float2(v.x, v.y)));
+                    if (FULL) y2 = fma2(make_float2(v.z, v.w), h[p], y2);
+                }
+                if (FULL) {
+                    if (me.in) st_f32<T>(py, fmaf(Dv, xv[k], y2.x + y2.y) * gate[k]);
+                    py += c.channels;
+                } else {
+                    steps += dl[k];
+                }
+            }
         }
+        if (t0 + TT < hi) stage.put(bc[buf ^ 1]);
     }
+    if (!me.in) return;
+    if (FULL) {
+        if (slot >= 0 && hi == end)
 #pragma unroll
-    for (int k = 0; k < LEN; ++k) {
-        float o = fmaf(Dv, ld_f32<T>(px + k * CB), k & 1 ? y2[k / 2].y : y2[k / 2].x);
-        if (c.z) o *= silu_v(ld_f32<T>(pz + k * CB));
-        if (k < mine) st_f32<T>(px + k * CB, o);
+            for (int n = 0; n < NP; ++n)
+                if (n < N) state[n] = n & 1 ? h[n / 2].y : h[n / 2].x;
+    } else {
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            if (n < N) carried[(size_t)n * c.channels] = n & 1 ? h[n / 2].y : h[n / 2].x;
+        sg.steps[(size_t)blockIdx.x * c.channels + d] = steps;
     }
 }
 
-template <typename T, int TL, int K>
-__global__ void __launch_bounds__(SEL_WARPS * 32, 2) sel_fwd_kernel(SelCall c, bool wide, bool wide_bc) {
-    using S = FwdShape<T, TL, K>;
-    using Rows = typename S::Rows;
-    using BC = typename S::BC;
-    constexpr int SEG = S::SEG, CB = S::CB;
-    extern __shared__ __align__(16) unsigned char smem[];
-    unsigned char *xs = smem, *ds = xs + Rows::BYTES, *zs = ds + Rows::BYTES;
-    uint32_t *bc = reinterpret_cast<uint32_t *>(zs + Rows::BYTES);
-    const int N = c.dstate;
-    float *As = reinterpret_cast<float *>(bc + N * BC::STATE_WORDS), *hs = As + CB * N;  // [n][channel]
-
-    const int i = blockIdx.x;
+// A thread per (sequence, state, channel) goes through the sequence's segments.
+__global__ void __launch_bounds__(128) sel_join_kernel(SelCall c, Segments sg, bool backwards) {
+    const int i = blockIdx.x, n = blockIdx.z, d = blockIdx.y * 128 + threadIdx.x, N = c.dstate;
     int lo, hi;
-    if (!seq_rows(c.seq, i, lo, hi) || lo == hi) return;  // the same for the whole block
-    const int per_group = c.channels / c.groups, tiles = (per_group + CB - 1) / CB;
-    const int g = blockIdx.y / tiles, c0 = g * per_group + (blockIdx.y % tiles) * CB;
-    const int cols = min(CB, (g + 1) * per_group - c0);
-    const int slot = c.state ? slot_of(c.seq.slots, c.seq.nslots, i, c.seq.dev_error) : -1;
-    const bool init = slot >= 0 && c.seq.has_init && c.seq.has_init[i];
-    float *st = c.state + (slot >= 0 ? ((size_t)slot * c.channels + c0) * N : 0);
-    for (int u = threadIdx.x; u < CB * N; u += SEL_WARPS * 32) {
-        const int ch = u / N, n = u - ch * N;
-        const bool in = ch < cols;
-        As[n * CB + ch] = in ? c.A[(size_t)c0 * N + u] * LOG2E : 0.f;
-        hs[n * CB + ch] = in && init ? st[u] : 0.f;
+    if (!seq_rows(c.seq, i, lo, hi) || lo == hi) return;
+    const int slot = !backwards && c.state ? slot_of(c.seq.slots, c.seq.nslots, i, c.seq.dev_error) : -1;
+    if (d >= c.channels) return;
+    const float A2 = c.A[(size_t)d * N + n] * LOG2E;
+    float h = slot >= 0 && c.seq.has_init && c.seq.has_init[i] ? c.state[((size_t)slot * c.channels + d) * N + n] : 0.f;
+    const int count = (hi - lo + sg.seg - 1) / sg.seg, s0 = lo / sg.seg + i;
+    const size_t step = (size_t)N * c.channels;
+    float *at = sg.state + (size_t)s0 * step + (size_t)n * c.channels + d;
+    const float *steps = sg.steps + (size_t)s0 * c.channels + d;
+    // the segment at the far end has neither an end state nor steps: nothing needs them
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) {
+        const int k = backwards ? count - 1 - j : j;
+        const bool more = j + 1 < count;
+        const float S = more ? at[k * step] : 0.f, w = more ? steps[(size_t)k * c.channels] : 0.f;
+        at[k * step] = h;
+        h = fmaf(ex2a(A2 * w), h, S);
     }
-    const int lane = threadIdx.x & 31, l = lane % TL, ch = (threadIdx.x >> 5) * S::CL + lane / TL;
-    const int chc = min(ch, cols - 1);
-    const float bias = c.dt_bias ? c.dt_bias[c0 + chc] : 0.f, Dv = c.D ? c.D[c0 + chc] : 0.f;
-    const T *x = static_cast<const T *>(c.x) + c0, *dt = static_cast<const T *>(c.dt) + c0,
-            *z = static_cast<const T *>(c.z) + c0;
-    const T *B = static_cast<const T *>(c.B) + g * N, *C = static_cast<const T *>(c.C) + g * N;
-    T *y = static_cast<T *>(c.y) + c0;
-
-    for (int t0 = lo, chunk = 0; t0 < hi; t0 += SEG, ++chunk) {
-        const int n = min(SEG, hi - t0), per_lane = (n + TL - 1) / TL, len = per_lane <= 4 ? 4 : per_lane <= 8 ? 8 : K;
-        Rows::fetch(xs, x + t0 * c.ld_x, c.ld_x, n, cols, len, wide);
-        Rows::fetch(ds, dt + t0 * c.ld_dt, c.ld_dt, n, cols, len, wide);
-        if (c.z) Rows::fetch(zs, z + t0 * c.ld_z, c.ld_z, n, cols, len, wide);
-        cp_commit();
-        BC::fetch(bc, B + t0 * c.ld_b, c.ld_b, C + t0 * c.ld_c, c.ld_c, n, N, len, wide_bc);
-        cp_wait<0>();
-        __syncthreads();
-        if (c.chunk_states) {  // SEG == SEL_CHUNK then
-            float *o = c.chunk_states + ((size_t)(lo / SEL_CHUNK + i + chunk) * c.channels + c0) * N;
-            for (int u = threadIdx.x; u < cols * N; u += SEL_WARPS * 32) o[u] = hs[(u % N) * CB + u / N];
-            __syncthreads();  // before hs moves on
-        }
-        const int mine = ch < cols ? max(0, min(len, n - l * len)) : 0;  // tokens of this lane
-        if (len == 4)
-            fwd_chunk<T, TL, K, 1>(c, xs, ds, zs, bc, As, hs, l, ch, mine, bias, Dv);
-        else if (len == 8)
-            fwd_chunk<T, TL, K, 2>(c, xs, ds, zs, bc, As, hs, l, ch, mine, bias, Dv);
-        else
-            fwd_chunk<T, TL, K, 4>(c, xs, ds, zs, bc, As, hs, l, ch, mine, bias, Dv);
-        __syncthreads();
-        Rows::flush(xs, y + (size_t)t0 * c.channels, c.channels, n, cols, len, wide);
-        __syncthreads();  // before the next chunk's copies
-    }
-    if (slot >= 0)
-        for (int u = threadIdx.x; u < cols * N; u += SEL_WARPS * 32) st[u] = hs[(u % N) * CB + u / N];
 }
 
 // One token per sequence, in place on the state.  A warp takes 32 channels.  Each lane
@@ -243,25 +238,21 @@ __global__ void __launch_bounds__(UPD_THREADS) sel_update_kernel(SelCall c, bool
     }
 }
 
-template <typename T, int TL, int K> cudaError_t run_fwd(const SelCall &c, cudaStream_t st) {
-    using S = FwdShape<T, TL, K>;
-    const size_t smem = S::smem(c.dstate), e = sizeof(T);
-    const int per_group = c.channels / c.groups;
-    const bool wide = rows_aligned(c.x, c.ld_x, e, 16) && rows_aligned(c.dt, c.ld_dt, e, 16) &&
-                      (!c.z || rows_aligned(c.z, c.ld_z, e, 16)) && rows_aligned(c.y, c.channels, e, 16) &&
-                      per_group * e % 16 == 0;
-    const bool wide_bc = c.dstate % 4 == 0 && rows_aligned(c.B, c.ld_b, e, 4 * e) && rows_aligned(c.C, c.ld_c, e, 4 * e);
-    cudaError_t err = cudaFuncSetAttribute(sel_fwd_kernel<T, TL, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err != cudaSuccess) return err;
-    const dim3 grid(c.seq.nseq, c.groups * ((per_group + S::CB - 1) / S::CB));
-    sel_fwd_kernel<T, TL, K><<<grid, SEL_WARPS * 32, smem, st>>>(c, wide, wide_bc);
-    return cudaGetLastError();
-}
+constexpr int FWD_WARPS_PER_SM = 16;
 
-template <typename T> cudaError_t pick_fwd(const SelCall &c, cudaStream_t st) {
-    const long long blocks = (long long)c.seq.nseq * ((c.channels + 31) / 32);
-    if (!c.chunk_states && c.dstate <= 16 && blocks < 148) return run_fwd<T, 32, 16>(c, st);
-    return run_fwd<T, 8, 16>(c, st);
+template <typename T> cudaError_t run_fwd(const SelCall &c, const Segments &sg, cudaStream_t st) {
+    const dim3 grid(sg.slots, channel_tiles<FWD_THREADS>(c));
+    const bool wide = wide_bc(c);
+    return with_states(c.dstate, [&](auto np) {
+        if (sg.seg != WHOLE) {
+            sel_fwd_kernel<T, np(), false><<<grid, FWD_THREADS, 0, st>>>(c, sg, wide);
+            cudaError_t e = cudaGetLastError();
+            if (e == cudaSuccess) e = launch_sel_join(c, sg, false, st);
+            if (e != cudaSuccess) return e;
+        }
+        sel_fwd_kernel<T, np(), true><<<grid, FWD_THREADS, 0, st>>>(c, sg, wide);
+        return cudaGetLastError();
+    });
 }
 
 template <typename T, int LP> cudaError_t run_update(const SelCall &c, int batch, cudaStream_t st) {
@@ -287,8 +278,22 @@ template <typename T> cudaError_t pick_update(const SelCall &c, int batch, cudaS
 
 }  // namespace
 
-cudaError_t launch_sel_varlen(const SelCall &c, cudaStream_t st) {
-    return c.bf16 ? pick_fwd<__nv_bfloat16>(c, st) : pick_fwd<float>(c, st);
+cudaError_t launch_sel_join(const SelCall &c, const Segments &s, bool backwards, cudaStream_t st) {
+    sel_join_kernel<<<dim3(c.seq.nseq, (c.channels + 127) / 128, c.dstate), 128, 0, st>>>(c, s, backwards);
+    return cudaGetLastError();
+}
+
+size_t sel_fwd_workspace(int tokens, int nseq, int channels, int dstate) {
+    const int seg = choose_seg(tokens, nseq, channels, FWD_WARPS_PER_SM);
+    return seg == WHOLE ? 0 : (size_t)seg_slots(tokens, nseq, seg) * channels * (dstate + 1) * sizeof(float);
+}
+
+cudaError_t launch_sel_varlen(const SelCall &c, float *ws, cudaStream_t st) {
+    Segments sg;
+    sg.seg = choose_seg(c.seq.tokens, c.seq.nseq, c.channels, FWD_WARPS_PER_SM);
+    sg.slots = seg_slots(c.seq.tokens, c.seq.nseq, sg.seg);
+    sg.state = ws, sg.steps = ws + (sg.seg == WHOLE ? 0 : (size_t)sg.slots * c.dstate * c.channels);
+    return c.bf16 ? run_fwd<__nv_bfloat16>(c, sg, st) : run_fwd<float>(c, sg, st);
 }
 cudaError_t launch_sel_update(const SelCall &c, int batch, cudaStream_t st) {
     return c.bf16 ? pick_update<__nv_bfloat16>(c, batch, st) : pick_update<float>(c, batch, st);

@@ -38,7 +38,8 @@ def declare_mixer(lib):
     sig("ssd_conv1d_bwd_workspace_size", _I, _I, _I, res=_SZ)
     sig("ssd_conv1d_bwd", _VP, _LL, *[_VP] * 9, *[_I] * 7, _VP, _SZ, _VP)
     sig("ssd_selective_scan_chunk_states", _I, _I, res=_SZ)
-    sig("ssd_selective_scan_varlen", sel, *[_VP] * 6, _I, _I, _I, _VP)
+    sig("ssd_selective_scan_workspace_size", *[_I] * 4, res=_SZ)
+    sig("ssd_selective_scan_varlen", sel, *[_VP] * 6, _I, _I, _I, _VP, _SZ, _VP)
     sig("ssd_selective_state_update", sel, _VP, _VP, _VP, _I, _I, _VP)
     sig("ssd_selective_scan_bwd_workspace_size", *[_I] * 5, res=_SZ)
     sig("ssd_selective_scan_bwd", sel, *[_VP] * 11, _I, _I, _VP, _SZ, _VP)
@@ -311,9 +312,11 @@ def ssd_selective_scan_varlen(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bia
             y = x.new_empty((n, d))
         kept = None
         if return_chunk_states:
-            kept = torch.empty((_size("ssd_selective_scan_chunk_states", n, nseq), d, N), dtype=_f32, device=dev)
+            kept = torch.empty((_size("ssd_selective_scan_chunk_states", n, nseq), N, d), dtype=_f32, device=dev)
+        nbytes = _size("ssd_selective_scan_workspace_size", n, nseq, d, N)
+        ws = _scratch(nbytes, dev)
         check(f(a, cu, sp, slp, hip, None if kept is None else kept.data_ptr(), _whole(y, "y", x.dtype, dev, (n, d)), n,
-                nseq, nslots, _raw_stream(dev.index)))
+                nseq, nslots, None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev.index)))
     return y, kept
 
 
@@ -343,7 +346,7 @@ def ssd_selective_scan_bwd(x, dt, A, B, C, cu_seqlens, dy, chunk_states, D=None,
     a, dev, n, d, G, N = _sel_args(x, dt, A, B, C, D, z, dt_bias, softplus)
     cu, nseq = _sequences(cu_seqlens, dev)
     gy = _whole(dy, "dy", x.dtype, dev, (n, d))
-    kept = _whole(chunk_states, "chunk_states", _f32, dev, (_size("ssd_selective_scan_chunk_states", n, nseq), d, N))
+    kept = _whole(chunk_states, "chunk_states", _f32, dev, (_size("ssd_selective_scan_chunk_states", n, nseq), N, d))
     with _on(dev, stream):
         out = {} if out is None else out
         shapes = dict(dx=((n, d), x.dtype, x), ddt=((n, d), x.dtype, dt), dz=((n, d), x.dtype, z), dB=((n, G, N), x.dtype, B),

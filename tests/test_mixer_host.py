@@ -86,7 +86,7 @@ SEL_REFUSALS = [
 @pytest.mark.parametrize("over,status,msg", SEL_REFUSALS)
 def test_scan_refusals(lib, over, status, msg):
     a = sel_args(**over)
-    for st in (lib.ssd_selective_scan_varlen(a, FAKE, None, None, None, None, FAKE, 10, 2, 0, None),
+    for st in (lib.ssd_selective_scan_varlen(a, FAKE, None, None, None, None, FAKE, 10, 2, 0, FAKE, 1 << 30, None),
                lib.ssd_selective_state_update(a, FAKE, None, FAKE, 10, 10, None),
                lib.ssd_selective_scan_bwd(a, FAKE, FAKE, FAKE, *[FAKE] * 8, 10, 2, FAKE, 1 << 40, None)):
         assert st == status and msg in ssd.ssd_last_error()
@@ -94,12 +94,12 @@ def test_scan_refusals(lib, over, status, msg):
 
 def test_scan_refusals_of_each_call(lib):
     a = sel_args()
-    varlen = lambda *, cu=FAKE, st=None, y=FAKE, n=10, nseq=2, nslots=0, kept=None: lib.ssd_selective_scan_varlen(  # noqa: E731
-        a, cu, st, None, None, kept, y, n, nseq, nslots, None)
+    varlen = lambda *, cu=FAKE, st=None, y=FAKE, n=10, nseq=2, nslots=0, kept=None, ws=FAKE: lib.ssd_selective_scan_varlen(  # noqa: E731
+        a, cu, st, None, None, kept, y, n, nseq, nslots, ws, 1 << 20, None)
     assert varlen(cu=None) == BAD and varlen(y=None) == BAD and varlen(n=-1) == BAD and varlen(y=OFF) == BAD
     assert varlen(st=FAKE, nslots=1) == BAD and "slots" in ssd.ssd_last_error()
     assert varlen(n=(1 << 31) - 1) == UNSUP
-    assert lib.ssd_selective_scan_varlen(None, FAKE, None, None, None, None, FAKE, 10, 2, 0, None) == BAD
+    assert lib.ssd_selective_scan_varlen(None, FAKE, None, None, None, None, FAKE, 10, 2, 0, FAKE, 1 << 30, None) == BAD
     update = lambda *, st=FAKE, y=FAKE, n=10, nslots=10: lib.ssd_selective_state_update(a, st, None, y, n, nslots, None)  # noqa: E731
     assert update(st=None) == BAD and update(y=None) == BAD and update(n=-1) == BAD and update(n=65536) == UNSUP and update(nslots=9) == BAD
 
@@ -112,7 +112,10 @@ def test_scan_refusals_of_each_call(lib):
     for k in ("cu", "dy", "kept", "dx", "ddt", "dB", "dC", "dA"):
         assert bwd(k) == BAD and "non-null" in ssd.ssd_last_error(), k
     assert bwd("dx", OFF) == BAD and bwd(ws=None) == WORK and bwd(wsb=64) == WORK
-    assert lib.ssd_selective_scan_chunk_states(300, 3) == 5 and lib.ssd_selective_scan_chunk_states(-1, 3) == ssd.SSD_WORKSPACE_INVALID
+    assert varlen(n=1 << 20, ws=None) == WORK and varlen(n=1 << 20) == WORK and varlen(ws=OFF) == BAD
+    assert lib.ssd_selective_scan_workspace_size(1 << 20, 2, 64, 16) > 1 << 20
+    assert lib.ssd_selective_scan_workspace_size(64 * 512, 64, 1024, 16) == 0
+    assert lib.ssd_selective_scan_chunk_states(300, 3) == 300 // 16 + 3 and lib.ssd_selective_scan_chunk_states(-1, 3) == ssd.SSD_WORKSPACE_INVALID
     assert lib.ssd_selective_scan_bwd_workspace_size(10, 2, 64, 3, 16) == ssd.SSD_WORKSPACE_INVALID
 
 
