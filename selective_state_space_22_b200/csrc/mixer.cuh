@@ -116,6 +116,23 @@ __device__ __forceinline__ float2 silu2(float2 v) {
     return mul2(v, make_float2(rcpa(d.x), rcpa(d.y)));
 }
 
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+    const float2 e = mul2(v, splat(-LOG2E)), d = add2(make_float2(ex2a(e.x), ex2a(e.y)), splat(1.f));
+    return make_float2(rcpa(d.x), rcpa(d.y));
+}
+__device__ __forceinline__ float2 softplus2(float2 v) {  // softplus_f of each
+    const float2 e = mul2(make_float2(fabsf(v.x), fabsf(v.y)), splat(-LOG2E));
+    const float2 t = make_float2(ex2a(e.x), ex2a(e.y)), d = add2(t, splat(2.f));
+    const float2 s = mul2(t, make_float2(rcpa(d.x), rcpa(d.y))), q = mul2(s, s);
+    float2 p = fma2(q, splat(1.f / 13.f), splat(1.f / 11.f));
+    p = fma2(q, p, splat(1.f / 9.f));
+    p = fma2(q, p, splat(1.f / 7.f));
+    p = fma2(q, p, splat(1.f / 5.f));
+    p = fma2(q, p, splat(1.f / 3.f));
+    p = fma2(q, p, splat(1.f));
+    return fma2(add2(s, s), p, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+}
+
 // V consecutive elements <-> floats, one access of V * sizeof(T) bytes where WIDE
 // (the caller has checked the alignment), else V accesses.
 template <typename T, int V, bool WIDE> __device__ __forceinline__ void load_v(const T *p, float (&v)[V]) {
@@ -200,7 +217,7 @@ struct SelCall {
     int softplus, channels, groups, dstate;
     Packed seq;
 };
-constexpr int SEL_CHUNK = 16;  // tokens between kept states
+constexpr int SEL_CHUNK = 8;  // tokens between kept states
 constexpr int SEL_MAX_DSTATE = 64;  // states of a channel in registers
 size_t sel_fwd_workspace(int tokens, int nseq, int channels, int dstate);
 cudaError_t launch_sel_varlen(const SelCall &c, float *ws, cudaStream_t st);

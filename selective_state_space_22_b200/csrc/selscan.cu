@@ -4,73 +4,106 @@
 //   h_t[n] = exp(delta_t A[n]) h_{t-1}[n] + delta_t x_t B_t[n],
 //   y_t = (sum_n C_t[n] h_t[n] + D x_t) silu(z_t)          per channel.
 //
-// A thread per channel, its states in registers, along a sequence or a segment of one
-// (selscan_seg.cuh): three packed operations and an exponential per state and token,
-// some forty more per token.  x, dt, z and y go straight between global memory and
-// registers (neighbouring lanes, neighbouring channels), four tokens ahead; B and C,
+// A thread per channel and 8 states, along a sequence or a segment of one
+// (selscan_seg.cuh): per state and token three packed operations to two states and an
+// exponential.  x, dt, z and y go straight between global memory and
+// registers (neighbouring lanes, neighbouring channels), eight tokens ahead; B and C,
 // which a block's channels share, through shared memory.  Bound by the exponential
 // unit (N + 4 operations per channel and token at 16 per SM and clock), then by issue.
-// A first form split the tokens of a chunk over the lanes of a warp, with one
-// exponential per state and token at any length; its scans over lanes and the second
-// walk they need left it at 352 us where this one takes KERNEL_TIME (64 x 512 tokens,
-// 1024 channels, 16 states).
+// Measured at 64 x 512 tokens, 1024 channels, 16 states: KERNEL_TIME.  A form that split the
+// tokens of a chunk over the lanes of a warp (one exponential per state and token at any
+// length, but scans over lanes and a second walk) took 352 us, all states in one thread 318 us,
+// two channels to a packed operation 290 us.
 #include "selscan_seg.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int FWD_THREADS = 64, AHEAD = 4;
+constexpr int AHEAD = 8;  // tokens at a time, and fetched ahead
+constexpr int FWD_BLOCKS_PER_SM = 8;
+
+template <int NP> struct FwdLanes {
+    static constexpr int NS = NP < 8 ? NP : 8, P = NS / 2, SPLIT = NP / NS, CHANS = 32 / SPLIT, OWN = AHEAD / SPLIT;
+    static constexpr int CH = SCAN_THREADS / SPLIT;  // channels of a block
+    static constexpr int TT = NP <= 16 ? 32 : 16;    // tokens of B and C at a time
+};
+
+// v[k] summed over the SPLIT lanes of a channel: a lane of part s ends with token
+// j SPLIT + s in v[j].
+template <int SPLIT, int K> __device__ __forceinline__ void sum_lanes(float (&v)[K], int part) {
+    constexpr int CHANS = 32 / SPLIT;
+#pragma unroll
+    for (int j = 0; j < K / SPLIT; ++j) {
+        float t[SPLIT];
+#pragma unroll
+        for (int u = 0; u < SPLIT; ++u) t[u] = v[j * SPLIT + u];
+#pragma unroll
+        for (int n = SPLIT / 2; n > 0; n /= 2)
+#pragma unroll
+            for (int u = 0; u < n; ++u)
+                t[u] = (part & n ? t[u + n] : t[u]) + __shfl_xor_sync(0xffffffffu, part & n ? t[u] : t[u + n], n * CHANS);
+        v[j] = t[0];
+    }
+}
 
 // FULL: y, kept states and the end state; else only what sel_join needs.
 template <typename T, int NP, bool FULL>
-__global__ void __launch_bounds__(FWD_THREADS) sel_fwd_kernel(SelCall c, Segments sg, bool wide) {
-    constexpr int P = NP / 2, TT = NP <= 16 ? 32 : 16;
-    using Stage = StageBC<T, NP, TT, FWD_THREADS>;
-    __shared__ __align__(16) float4 bc[2][Stage::BYTES / 16];
+__global__ void __launch_bounds__(SCAN_THREADS, FWD_BLOCKS_PER_SM) sel_fwd_kernel(SelCall c, Segments sg, bool wide) {
+    using L = FwdLanes<NP>;
+    constexpr int P = L::P, SPLIT = L::SPLIT, CHANS = L::CHANS, OWN = L::OWN, TT = L::TT;
+    using Stage = StageBC<T, NP, TT, false>;
+    __shared__ __align__(16) float4 bc[2][TT * NP / 2];
     int i, first, lo, hi, end;
     if (!segment(c.seq, sg.seg, blockIdx.x, i, first, lo, hi, end)) return;  // the same for the whole block
     if (!FULL && hi == end) return;  // nothing follows
-    const Mine me = my_channel<FWD_THREADS>(c, blockIdx.y);
-    const int N = c.dstate, d = me.channel, slot = FULL && c.state ? slot_of(c.seq.slots, c.seq.nslots, i, c.seq.dev_error) : -1;
-    const T *B = static_cast<const T *>(c.B) + me.group * N + lo * c.ld_b, *C = static_cast<const T *>(c.C) + me.group * N + lo * c.ld_c;
+    const int N = c.dstate, lane = threadIdx.x & 31, part = lane / CHANS, n0 = part * L::NS;
+    const int per_group = c.channels / c.groups, tiles = (per_group + L::CH - 1) / L::CH, group = blockIdx.y / tiles;
+    const int at = blockIdx.y % tiles * L::CH + (threadIdx.x >> 5) * CHANS + lane % CHANS;
+    const bool mine = at < per_group;
+    const int d = group * per_group + min(at, per_group - 1);  // threads past the group follow along on its last channel
+    const T *B = static_cast<const T *>(c.B) + group * N + lo * c.ld_b, *C = static_cast<const T *>(c.C) + group * N + lo * c.ld_c;
     Stage stage;
     stage.load(B, c.ld_b, C, c.ld_c, min(TT, hi - lo), N, wide);
-    float2 A2[P], h[P];
+    // the lane's next tokens: part, part + SPLIT, ..
+    int row = lo + part;
+    const T *px = static_cast<const T *>(c.x) + row * c.ld_x + d, *pd = static_cast<const T *>(c.dt) + row * c.ld_dt + d;
+    const T *pz = static_cast<const T *>(c.z) + (c.z ? row * c.ld_z + d : 0);
+    T *py = static_cast<T *>(c.y) + (size_t)row * c.channels + d;
+    T nx[OWN], nd[OWN], nz[OWN];
+    auto fetch = [&] {
+#pragma unroll
+        for (int j = 0; j < OWN; ++j) {
+            if (row < hi) {
+                nx[j] = *px, nd[j] = *pd;
+                if (FULL && c.z) nz[j] = *pz;
+            }
+            row += SPLIT, px += SPLIT * c.ld_x, pd += SPLIT * c.ld_dt;
+            if (FULL) pz += SPLIT * c.ld_z;
+        }
+    };
+    fetch();
+    const int slot = FULL && c.state ? slot_of(c.seq.slots, c.seq.nslots, i, c.seq.dev_error) : -1;
     float *const state = c.state + (slot >= 0 ? ((size_t)slot * c.channels + d) * N : 0);
     const bool init = slot >= 0 && c.seq.has_init && c.seq.has_init[i] && sg.seg == WHOLE;
-    float *const carried = sg.state + ((size_t)blockIdx.x * N) * c.channels + d;
+    float *const carried = sg.state + (size_t)blockIdx.x * N * c.channels + d;  // [state][channel]
     auto load_h = [&](int n) {
         if (n >= N) return 0.f;
         if (FULL && sg.seg != WHOLE) return carried[(size_t)n * c.channels];
         return init ? state[n] : 0.f;
     };
+    auto load_A = [&](int n) { return n < N ? c.A[(size_t)d * N + n] * LOG2E : 0.f; };
+    float2 A2[P], h[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-        A2[p] = make_float2(2 * p < N ? c.A[(size_t)d * N + 2 * p] * LOG2E : 0.f, 2 * p + 1 < N ? c.A[(size_t)d * N + 2 * p + 1] * LOG2E : 0.f);
-        h[p] = make_float2(load_h(2 * p), load_h(2 * p + 1));
+        A2[p] = make_float2(load_A(n0 + 2 * p), load_A(n0 + 2 * p + 1));
+        h[p] = make_float2(load_h(n0 + 2 * p), load_h(n0 + 2 * p + 1));
     }
-    const float bias = c.dt_bias ? c.dt_bias[d] : 0.f, Dv = c.D ? c.D[d] : 0.f;
-    const T *px = static_cast<const T *>(c.x) + lo * c.ld_x + d, *pd = static_cast<const T *>(c.dt) + lo * c.ld_dt + d;
-    const T *pz = static_cast<const T *>(c.z) + (c.z ? lo * c.ld_z + d : 0);
-    T *py = static_cast<T *>(c.y) + (size_t)lo * c.channels + d;
-    T nx[AHEAD], nd[AHEAD], nz[AHEAD];
-    int left = hi - lo;  // tokens not yet fetched
-    auto fetch = [&] {
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            if (k < left) {
-                nx[k] = *px, nd[k] = *pd;
-                if (FULL && c.z) nz[k] = *pz, pz += c.ld_z;
-                px += c.ld_x, pd += c.ld_dt;
-            }
-        }
-        left -= AHEAD;
-    };
-    fetch();
-    stage.put(bc[0]);
+    const float bias = c.dt_bias ? c.dt_bias[d] : 0.f, D = c.D ? c.D[d] : 0.f;
     float steps = 0.f;
     float *kept = nullptr;
-    if (FULL && c.chunk_states) kept = c.chunk_states + ((size_t)(first / SEL_CHUNK + i + (lo - first) / SEL_CHUNK) * N) * c.channels + d;
+    if (FULL && c.chunk_states)
+        kept = c.chunk_states + ((size_t)(first / SEL_CHUNK + i + (lo - first) / SEL_CHUNK) * N + n0) * c.channels + d;
+    stage.put(bc[0]);
     for (int t0 = lo, buf = 0; t0 < hi; t0 += TT, buf ^= 1) {
         const int nt = min(TT, hi - t0);
         B += TT * c.ld_b, C += TT * c.ld_c;
@@ -78,56 +111,77 @@ __global__ void __launch_bounds__(FWD_THREADS) sel_fwd_kernel(SelCall c, Segment
         __syncthreads();  // bc[buf] is written, and nobody reads bc[buf ^ 1] any more
 #pragma unroll 1
         for (int t = 0; t < nt; t += AHEAD) {
-            float dl[AHEAD], xv[AHEAD], gate[AHEAD];
+            // the lane's tokens; one past the end is a step of nothing
+            float dl[OWN], u[OWN], xv[OWN], gate[OWN];
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                xv[k] = ld_f32<T>(&nx[k]);
-                dl[k] = ld_f32<T>(&nd[k]) + bias;
-                if (c.softplus) dl[k] = softplus_f(dl[k]);
-                if (FULL) gate[k] = c.z ? silu_v(ld_f32<T>(&nz[k])) : 1.f;
+            for (int j = 0; j < OWN; ++j) {
+                const bool in = t + j * SPLIT + part < nt;
+                xv[j] = ld_f32<T>(&nx[j]);
+                dl[j] = ld_f32<T>(&nd[j]) + bias;
+                if (c.softplus) dl[j] = softplus_f(dl[j]);
+                if (FULL && c.z) gate[j] = silu_v(ld_f32<T>(&nz[j]));
+                u[j] = in ? dl[j] * xv[j] : 0.f, dl[j] = in ? dl[j] : 0.f;
+                if (!FULL) steps += dl[j];
             }
             fetch();
-            if (FULL && kept && (t0 - first + t) % SEL_CHUNK == 0) {
-                if (me.in)
+            if (FULL && kept) {
+                static_assert(SEL_CHUNK == AHEAD, "a state is kept before every step of this loop");
+                if (mine)
 #pragma unroll
-                    for (int n = 0; n < NP; ++n)
-                        if (n < N) kept[(size_t)n * c.channels] = n & 1 ? h[n / 2].y : h[n / 2].x;
+                    for (int k = 0; k < L::NS; ++k)
+                        if (n0 + k < N) kept[(size_t)k * c.channels] = k & 1 ? h[k / 2].y : h[k / 2].x;
                 kept += (size_t)N * c.channels;
             }
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                if (t + k >= nt) break;
-                const float2 d2 = splat(dl[k]), u2 = splat(dl[k] * xv[k]);
+            float y[AHEAD];
+            const float4 *q = bc[buf] + (t * NP + n0) / 2;
+            auto token = [&](int k) {
+                const float ds = SPLIT == 1 ? dl[k / SPLIT] : __shfl_sync(0xffffffffu, dl[k / SPLIT], lane % CHANS + k % SPLIT * CHANS);
+                const float us = SPLIT == 1 ? u[k / SPLIT] : __shfl_sync(0xffffffffu, u[k / SPLIT], lane % CHANS + k % SPLIT * CHANS);
                 float2 y2 = make_float2(0.f, 0.f);
-                const float4 *q = bc[buf] + (t + k) * P;
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
-                    const float4 v = q[p];
-                    const float2 arg = mul2(d2, A2[p]);
-                    h[p] = fma2(make_float2(ex2a(arg.x), ex2a(arg.y)), h[p], mul2(u2, make_float2(v.x, v.y)));
+                    const float4 v = q[k * (NP / 2) + p];
+                    const float2 arg = mul2(splat(ds), A2[p]);
+                    h[p] = fma2(make_float2(ex2a(arg.x), ex2a(arg.y)), h[p], mul2(splat(us), make_float2(v.x, v.y)));
                     if (FULL) y2 = fma2(make_float2(v.z, v.w), h[p], y2);
                 }
-                if (FULL) {
-                    if (me.in) st_f32<T>(py, fmaf(Dv, xv[k], y2.x + y2.y) * gate[k]);
-                    py += c.channels;
-                } else {
-                    steps += dl[k];
+                y[k] = y2.x + y2.y;
+            };
+#pragma unroll
+            for (int k = 0; k < AHEAD / 2; ++k) token(k);
+            if (t + AHEAD / 2 < nt) {
+#pragma unroll
+                for (int k = AHEAD / 2; k < AHEAD; ++k) token(k);
+            } else {
+#pragma unroll
+                for (int k = AHEAD / 2; k < AHEAD; ++k) y[k] = 0.f;
+            }
+            if (FULL) {
+                sum_lanes<SPLIT>(y, part);
+#pragma unroll
+                for (int j = 0; j < OWN; ++j) {
+                    float o = fmaf(D, xv[j], y[j]);
+                    if (c.z) o *= gate[j];
+                    if (mine && t + j * SPLIT + part < nt) st_f32<T>(py, o);
+                    py += (size_t)SPLIT * c.channels;
                 }
             }
         }
         if (t0 + TT < hi) stage.put(bc[buf ^ 1]);
     }
-    if (!me.in) return;
     if (FULL) {
-        if (slot >= 0 && hi == end)
+        if (slot >= 0 && hi == end && mine)
 #pragma unroll
-            for (int n = 0; n < NP; ++n)
-                if (n < N) state[n] = n & 1 ? h[n / 2].y : h[n / 2].x;
+            for (int k = 0; k < L::NS; ++k)
+                if (n0 + k < N) state[n0 + k] = k & 1 ? h[k / 2].y : h[k / 2].x;
     } else {
+        if (mine)
 #pragma unroll
-        for (int n = 0; n < NP; ++n)
-            if (n < N) carried[(size_t)n * c.channels] = n & 1 ? h[n / 2].y : h[n / 2].x;
-        sg.steps[(size_t)blockIdx.x * c.channels + d] = steps;
+            for (int k = 0; k < L::NS; ++k)
+                if (n0 + k < N) carried[(size_t)(n0 + k) * c.channels] = k & 1 ? h[k / 2].y : h[k / 2].x;
+#pragma unroll
+        for (int o = CHANS; o < 32; o *= 2) steps += __shfl_xor_sync(0xffffffffu, steps, o);
+        if (mine && part == 0) sg.steps[(size_t)blockIdx.x * c.channels + d] = steps;
     }
 }
 
@@ -145,13 +199,21 @@ __global__ void __launch_bounds__(128) sel_join_kernel(SelCall c, Segments sg, b
     float *at = sg.state + (size_t)s0 * step + (size_t)n * c.channels + d;
     const float *steps = sg.steps + (size_t)s0 * c.channels + d;
     // the segment at the far end has neither an end state nor steps: nothing needs them
-#pragma unroll 4
-    for (int j = 0; j < count; ++j) {
-        const int k = backwards ? count - 1 - j : j;
-        const bool more = j + 1 < count;
-        const float S = more ? at[k * step] : 0.f, w = more ? steps[(size_t)k * c.channels] : 0.f;
-        at[k * step] = h;
-        h = fmaf(ex2a(A2 * w), h, S);
+    constexpr int BATCH = 8;  // loads in flight
+    for (int j0 = 0; j0 < count; j0 += BATCH) {
+        float S[BATCH], w[BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const int j = j0 + u, k = backwards ? count - 1 - j : j;
+            const bool more = j + 1 < count;
+            S[u] = more ? at[k * step] : 0.f, w[u] = more ? steps[(size_t)k * c.channels] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const int j = j0 + u, k = backwards ? count - 1 - j : j;
+            if (j < count) at[k * step] = h;
+            h = fmaf(ex2a(A2 * w[u]), h, S[u]);
+        }
     }
 }
 
@@ -240,18 +302,20 @@ __global__ void __launch_bounds__(UPD_THREADS) sel_update_kernel(SelCall c, bool
 
 constexpr int FWD_WARPS_PER_SM = 16;
 
+template <typename T, int NP, bool FULL> cudaError_t run_pass(const SelCall &c, const Segments &sg, cudaStream_t st) {
+    constexpr int CH = FwdLanes<NP>::CH;
+    const dim3 grid(sg.slots, c.groups * ((c.channels / c.groups + CH - 1) / CH));
+    sel_fwd_kernel<T, NP, FULL><<<grid, SCAN_THREADS, 0, st>>>(c, sg, Access(c).bc);
+    return cudaGetLastError();
+}
 template <typename T> cudaError_t run_fwd(const SelCall &c, const Segments &sg, cudaStream_t st) {
-    const dim3 grid(sg.slots, channel_tiles<FWD_THREADS>(c));
-    const bool wide = wide_bc(c);
     return with_states(c.dstate, [&](auto np) {
         if (sg.seg != WHOLE) {
-            sel_fwd_kernel<T, np(), false><<<grid, FWD_THREADS, 0, st>>>(c, sg, wide);
-            cudaError_t e = cudaGetLastError();
+            cudaError_t e = run_pass<T, np(), false>(c, sg, st);
             if (e == cudaSuccess) e = launch_sel_join(c, sg, false, st);
             if (e != cudaSuccess) return e;
         }
-        sel_fwd_kernel<T, np(), true><<<grid, FWD_THREADS, 0, st>>>(c, sg, wide);
-        return cudaGetLastError();
+        return run_pass<T, np(), true>(c, sg, st);
     });
 }
 

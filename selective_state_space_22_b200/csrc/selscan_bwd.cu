@@ -7,88 +7,90 @@
 //   ddelta_t = x_t du_t + sum_n A q_t,  dx_t = delta_t du_t + D dp_t,  dD = sum_t dp_t x_t
 //   dz_t = dy_t p_t silu'(z_t),  ddt_t = ddelta_t softplus'(dt_t + bias),  dbias = sum_t ddt_t.
 //
-// A thread per channel walks its sequence (or segment, selscan_seg.cuh) backwards, in
+// A thread takes two channels and 8 states and walks its sequence (or segment,
+// selscan_seg.cuh) backwards, in
 // chunks of SEL_CHUNK tokens that start where the forward kept the states, and a chunk
-// in two halves of SUB tokens.  For each half and pair of states it runs the
+// in two halves of SUB tokens.  For each half and state it runs the
 // recurrence forwards (a_t and h_{t-1} stay in registers, so the backward walk takes no
-// exponential) and then backwards, two states to a packed operation; the second half
+// exponential) and then backwards, both channels in one packed operation; the second half
 // starts from a state formed again from the first half's tokens, which costs half an
-// exponential per state and token and halves the states to keep.  Per state and token:
-// 7 operations, half of an extra forward step, 2 for the sums over channels.
+// exponential per state and token and halves the states to keep.
 // dB and dC are summed over a warp's channels by matrix instructions (ChannelSum), over
 // the block's warps in shared memory, and over blocks by sel_bwd_sum, all in a fixed
-// order.  Bound by issue.  A first form split a chunk's tokens over the lanes of a warp
-// like the forward's; its scans, its scalar chains and one barrier per state left it at
-// 1428 us where this one takes KERNEL_TIME (64 x 512 tokens, 1024 channels, 16 states).
+// order.  Bound by issue and latency: the registers of a half (step, input and upstream
+// gradient of 8 tokens, three sums for each, a_t and h_{t-1}) leave 12 warps to an SM.
+// Measured at 64 x 512 tokens, 1024 channels, 16 states: KERNEL_TIME.  A form that split a
+// chunk's tokens over the lanes of a warp took 1428 us, one with a channel per thread and
+// its states paired 1490 us (each step, input and gradient held twice, spilled).
 #include "selscan_seg.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int SUB = 8;
+constexpr int SUB = GROUP, BWD_BLOCKS_PER_SM = 8;
 static_assert(SEL_CHUNK == 2 * SUB, "a chunk is two halves");
 
-// Sums over the 32 channels of a warp by matrix instructions: D[value][lane/4] +=
-// A[value][k] B[k][lane/4], where B holds the lanes' values as they are (k: the four
-// lanes of a group, times two registers) and A is ones for the k of one value and zero
-// elsewhere; two shuffles and three additions are left for the eight groups.  Sixteen
-// values take 8 instructions and those, where shuffles that halve the values took 124.
+// Sums over a warp's channels by matrix instructions: D[lane/4][c] += A[lane/4][k] B[k][c],
+// where A holds four values of every lane as they are (k: the four lanes of a group, times
+// two registers; two rows of A per group) and B is ones where k and c belong together.  An
+// instruction thus adds each of the four values over the four lanes of a group; the
+// sums of instruction i land in the lanes with lane%4 = i.  Four instructions (the
+// gradients of B and C, four tokens each, of two states) fill D, and three shuffles that
+// halve the values add the groups of a part (the lanes that hold the same states).
 //   float32: each value goes in as two tf32 parts, its first 11 bits and the next 11, so
 //   that it keeps 2^-22; the sums are float32.
-//   bf16: the first part alone.  A product then loses what lies past 11 bits (below
+//   bf16: the first part alone.  A value then loses what lies past 11 bits (below
 //   2^-10 of it, a quarter of a step of the bf16 gradient it goes into); the sums are
 //   float32 all the same.
-template <typename T> struct ChannelSum {
-    uint32_t one[8];  // row lane/4 of A is all ones for value i (mod 8)
-    __device__ __forceinline__ explicit ChannelSum(int lane) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) one[i] = (lane >> 2) == i ? 0x3f800000u : 0u;
-    }
-    static __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, float b0, float b1) {
+template <typename T, int SPLIT> struct ChannelSum {
+    static constexpr int GROUPS = 8 / SPLIT;  // of a part
+    float d[4];
+    __device__ __forceinline__ void clear() { d[0] = d[1] = d[2] = d[3] = 0.f; }
+    static __device__ __forceinline__ void mma(float (&d)[4], const float (&v)[4], float b0, float b1) {
         asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+            : "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+              "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
     }
-    // Lanes 0 and 1 of each group of four end with the warp's sum of value lane/4 and
-    // lane/4 + 8, where value 2 i is v[i].x and value 2 i + 1 is v[i].y.
-    __device__ __forceinline__ float operator()(const float2 (&v)[8], int lane) const {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};  // rows lane/4 and lane/4 + 8, columns 2 (lane%4) and + 1
+    __device__ __forceinline__ void add(const float (&v)[4], int i, int lane) {
+        const float b0 = (lane >> 2) == 2 * i ? 1.f : 0.f, b1 = (lane >> 2) == 2 * i + 1 ? 1.f : 0.f;
+        if constexpr (sizeof(T) == 4) {
+            float x[4], y[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t p = one[(2 * i) & 7], q = one[(2 * i + 1) & 7];
-            const uint32_t a0 = i < 4 ? p : 0u, a1 = i < 4 ? 0u : p, a2 = i < 4 ? q : 0u, a3 = i < 4 ? 0u : q;
-            if constexpr (sizeof(T) == 4) {
-                const float x = __uint_as_float(__float_as_uint(v[i].x) & 0xffffe000u), y = __uint_as_float(__float_as_uint(v[i].y) & 0xffffe000u);
-                mma(d, a0, a1, a2, a3, x, y);
-                mma(d, a0, a1, a2, a3, v[i].x - x, v[i].y - y);
-            } else {
-                mma(d, a0, a1, a2, a3, v[i].x, v[i].y);
-            }
+            for (int k = 0; k < 4; ++k) x[k] = __uint_as_float(__float_as_uint(v[k]) & 0xffffe000u), y[k] = v[k] - x[k];
+            mma(d, x, b0, b1);
+            mma(d, y, b0, b1);
+        } else {
+            mma(d, v, b0, b1);
         }
-        const float s0 = d[0] + d[1], s1 = d[2] + d[3];
-        const float s = (lane & 1 ? s1 : s0) + __shfl_xor_sync(0xffffffffu, lane & 1 ? s0 : s1, 1);
-        return s + __shfl_xor_sync(0xffffffffu, s, 2);
+    }
+    // Instruction lane%4's sums over the part: out(value, sum) for the values this lane
+    // ends with.  d[0..3] are the group's sums of values 0, 2, 1, 3.
+    template <typename F> __device__ __forceinline__ void finish(int lane, F &&out) const {
+        auto half = [&](float a, float b, bool second, int mask) {  // the kept one, with the other lane's added
+            return (second ? b : a) + __shfl_xor_sync(0xffffffffu, second ? a : b, mask);
+        };
+        constexpr int top = GROUPS == 8 ? 16 : GROUPS == 4 ? 8 : 4;
+        const bool odd = lane & top;  // keeps values 1 and 3
+        const float a = half(d[0], d[2], odd, top), b = half(d[1], d[3], odd, top);
+        if constexpr (GROUPS == 2) {
+            out(odd ? 1 : 0, a), out(odd ? 3 : 2, b);
+        } else {
+            const bool upper = lane & (top / 2);
+            float s = half(a, b, upper, top / 2);
+            if (GROUPS == 8) s += __shfl_xor_sync(0xffffffffu, s, 4);
+            if (GROUPS == 4 || !(lane & 4)) out((odd ? 1 : 0) + (upper ? 2 : 0), s);
+        }
     }
 };
 
-__device__ __forceinline__ void cp16(void *smem, const void *gmem) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem)
-                 : "memory");
-}
-__device__ __forceinline__ void cp4(void *smem, const void *gmem) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem) : "memory");
-}
-__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-template <int NP> constexpr int bwd_threads() { return NP <= 32 ? 128 : 64; }
-
 template <typename T, int NP> struct BwdShared {
-    static constexpr int THREADS = bwd_threads<NP>(), P = NP / 2, WARPS = THREADS / 32;
-    T x[SEL_CHUNK][THREADS], dt[SEL_CHUNK][THREADS], z[SEL_CHUNK][THREADS], dy[SEL_CHUNK][THREADS];
-    float4 bc[SEL_CHUNK * P];
-    float2 A2[P][THREADS], G[P][THREADS], dA[P][THREADS], hm[P][THREADS];  // hm: the state before the second half
-    float h0[NP][THREADS];                                                // the state before the chunk
-    float part[WARPS][SUB][2][NP];                                        // a warp's sums: [token][dB, dC][state]
+    static constexpr int NS = Lanes<NP>::NS, WARPS = SCAN_THREADS / 32, CH = WARPS * Lanes<NP>::CH;
+    T x[SEL_CHUNK][CH], dt[SEL_CHUNK][CH], z[SEL_CHUNK][CH], dy[SEL_CHUNK][CH];
+    float4 bc[SEL_CHUNK * NP];
+    float2 A2[NS][SCAN_THREADS], G[NS][SCAN_THREADS], dA[NS][SCAN_THREADS];
+    float2 h0[NS][SCAN_THREADS], hm[NS][SCAN_THREADS];  // the states before the chunk and before its second half
+    float part[WARPS][SUB][2][NP];                      // a warp's sums: [token][dB, dC][state]
 };
 
 struct Parts {   // workspace
@@ -97,177 +99,194 @@ struct Parts {   // workspace
     float *d;    // [slots][2][channels]: dD, dbias
 };
 
-// n rows of `cols` channels into [SEL_CHUNK][THREADS]; wide: aligned 16-byte pieces
-template <typename T, int THREADS>
-__device__ __forceinline__ void fetch_rows(T (*to)[THREADS], const T *src, long long ld, int n, int cols, bool wide) {
-    if (wide) {
-        constexpr int E = 16 / (int)sizeof(T), PER = THREADS / E;
-        for (int u = threadIdx.x; u < n * PER; u += THREADS) {
-            const int r = u / PER, k = u % PER * E;
-            if (k < cols) cp16(&to[r][k], src + r * ld + k);
-        }
-    } else if ((int)threadIdx.x < cols) {
-        for (int r = 0; r < n; ++r) to[r][threadIdx.x] = src[r * ld + threadIdx.x];
-    }
-}
-
 template <typename T, int NP>
-__global__ void __launch_bounds__(bwd_threads<NP>(), NP <= 16 ? 3 : 1) sel_bwd_kernel(SelCall c, Segments sg, Parts parts, bool wide,
-                                                                             bool wide_states) {
+__global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kernel(SelCall c, Segments sg, Parts parts, Access ok) {
     using Sh = BwdShared<T, NP>;
-    constexpr int P = NP / 2, THREADS = Sh::THREADS;
+    using L = Lanes<NP>;
+    constexpr int NS = L::NS, SPLIT = L::SPLIT, PAIRS = L::PAIRS, CH = Sh::CH, OWN = SUB / SPLIT;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Sh &sh = *reinterpret_cast<Sh *>(smem_raw);
-    const Mine me = my_channel<THREADS>(c, blockIdx.y);
-    const int N = c.dstate, d = me.channel, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Mine me = my_channels<NP>(c, blockIdx.y);
+    const int N = c.dstate, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = lane / PAIRS, pair = lane % PAIRS, n0 = part * NS;
+    const int ch = 2 * (warp * PAIRS + pair);  // of the block's
     const size_t step = (size_t)N * c.channels;
-    float *const pa = parts.a + blockIdx.x * step + d, *const pd_ = parts.d + (size_t)blockIdx.x * 2 * c.channels + d;
+    float *const pa = parts.a + blockIdx.x * step, *const pdd = parts.d + (size_t)blockIdx.x * 2 * c.channels;
+    const float2 zero = make_float2(0.f, 0.f);
     int i, first, lo, hi, end;
     if (!segment(c.seq, sg.seg, blockIdx.x, i, first, lo, hi, end)) {  // the same for the whole block
-        if (me.in) {
-            for (int n = 0; n < N; ++n) pa[(size_t)n * c.channels] = 0.f;
-            pd_[0] = pd_[c.channels] = 0.f;
-        }
+        for (int k = 0; k < NS; ++k)
+            if (n0 + k < N) store_two<float>(pa + (size_t)(n0 + k) * c.channels, zero, me, ok.state);
+        if (part == 0) store_two<float>(pdd, zero, me, ok.state), store_two<float>(pdd + c.channels, zero, me, ok.state);
         return;
     }
-    const int per_group = c.channels / c.groups, tiles = (per_group + THREADS - 1) / THREADS;
-    const int t_first = me.group * per_group + blockIdx.y % tiles * THREADS, t_cols = min(THREADS, (me.group + 1) * per_group - t_first);
-    const float bias = c.dt_bias ? c.dt_bias[d] : 0.f, Dv = c.D ? c.D[d] : 0.f;
-    const ChannelSum<T> channel_sum(lane);
-    for (int p = 0; p < P; ++p) {
-        const int n = 2 * p;
-        sh.A2[p][tid] = make_float2(n < N ? c.A[(size_t)d * N + n] * LOG2E : 0.f, n + 1 < N ? c.A[(size_t)d * N + n + 1] * LOG2E : 0.f);
-        sh.dA[p][tid] = make_float2(0.f, 0.f);
-        float2 G = make_float2(0.f, 0.f);
-        if (sg.seg != WHOLE) {
-            const float *from = sg.state + blockIdx.x * step + d;
-            if (n < N) G.x = from[(size_t)n * c.channels];
-            if (n + 1 < N) G.y = from[(size_t)(n + 1) * c.channels];
+    const int per_group = c.channels / c.groups, tiles = (per_group + CH - 1) / CH;
+    const int t_first = me.group * per_group + blockIdx.y % tiles * CH, t_cols = min(CH, (me.group + 1) * per_group - t_first);
+    const float2 bias = c.dt_bias ? make_float2(c.dt_bias[me.c0], c.dt_bias[me.c1]) : zero;
+    const float2 D = c.D ? make_float2(c.D[me.c0], c.D[me.c1]) : zero;
+    for (int k = 0; k < NS; ++k) {
+        const int n = n0 + k;
+        float2 A2 = zero, G = zero;
+        if (n < N) {
+            A2 = make_float2(c.A[(size_t)me.c0 * N + n] * LOG2E, c.A[(size_t)me.c1 * N + n] * LOG2E);
+            const float *from = sg.state + blockIdx.x * step + (size_t)n * c.channels;
+            if (sg.seg != WHOLE) G = make_float2(from[me.c0], from[me.c1]);
         }
-        sh.G[p][tid] = G;
+        sh.A2[k][tid] = A2, sh.G[k][tid] = G, sh.dA[k][tid] = sh.h0[k][tid] = zero;
     }
-    for (int n = N; n < NP; ++n) sh.h0[n][tid] = 0.f;
-    float dD = 0.f, dbias = 0.f;
-    StageBC<T, NP, SEL_CHUNK, THREADS> stage;
+    float2 dD = zero, dbias = zero;
+    StageBC<T, NP, SEL_CHUNK, true> stage;
     const T *B = static_cast<const T *>(c.B) + me.group * N, *C = static_cast<const T *>(c.C) + me.group * N;
     const int c_first = (lo - first) / SEL_CHUNK, c_last = (hi - 1 - first) / SEL_CHUNK;
-    const float *kept = c.chunk_states + (size_t)(first / SEL_CHUNK + i) * step + d;
+    const float *kept = c.chunk_states + (size_t)(first / SEL_CHUNK + i) * step;
     {
         const int t0 = first + c_last * SEL_CHUNK;
-        stage.load(B + t0 * c.ld_b, c.ld_b, C + t0 * c.ld_c, c.ld_c, min(SEL_CHUNK, hi - t0), N, wide_states);
+        stage.load(B + t0 * c.ld_b, c.ld_b, C + t0 * c.ld_c, c.ld_c, min(SEL_CHUNK, hi - t0), N, ok.bc);
     }
     for (int chunk = c_last; chunk >= c_first; --chunk) {
         const int t0 = first + chunk * SEL_CHUNK, n = min(SEL_CHUNK, hi - t0);
         __syncthreads();  // the chunk before has been read
-        fetch_rows<T, THREADS>(sh.x, static_cast<const T *>(c.x) + t0 * c.ld_x + t_first, c.ld_x, n, t_cols, wide);
-        fetch_rows<T, THREADS>(sh.dt, static_cast<const T *>(c.dt) + t0 * c.ld_dt + t_first, c.ld_dt, n, t_cols, wide);
-        if (c.z) fetch_rows<T, THREADS>(sh.z, static_cast<const T *>(c.z) + t0 * c.ld_z + t_first, c.ld_z, n, t_cols, wide);
-        fetch_rows<T, THREADS>(sh.dy, static_cast<const T *>(c.dy) + (size_t)t0 * c.channels + t_first, c.channels, n, t_cols, wide);
-        for (int s = 0; s < N; ++s) cp4(&sh.h0[s][tid], kept + chunk * step + (size_t)s * c.channels);
+        fetch_rows<T, CH>(sh.x, static_cast<const T *>(c.x) + t0 * c.ld_x + t_first, c.ld_x, n, t_cols, ok.wide);
+        fetch_rows<T, CH>(sh.dt, static_cast<const T *>(c.dt) + t0 * c.ld_dt + t_first, c.ld_dt, n, t_cols, ok.wide);
+        if (c.z) fetch_rows<T, CH>(sh.z, static_cast<const T *>(c.z) + t0 * c.ld_z + t_first, c.ld_z, n, t_cols, ok.wide);
+        fetch_rows<T, CH>(sh.dy, static_cast<const T *>(c.dy) + (size_t)t0 * c.channels + t_first, c.channels, n, t_cols, ok.wide);
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+            if (n0 + k >= N) continue;
+            const float *from = kept + chunk * step + (size_t)(n0 + k) * c.channels;
+            if (ok.state) {
+                cp8(&sh.h0[k][tid], from + me.c0);
+            } else {
+                cp4(&sh.h0[k][tid].x, from + me.c0);
+                cp4(&sh.h0[k][tid].y, from + me.c1);
+            }
+        }
         stage.put(sh.bc);
         if (chunk > c_first) {
             const int tp = t0 - SEL_CHUNK;
-            stage.load(B + tp * c.ld_b, c.ld_b, C + tp * c.ld_c, c.ld_c, SEL_CHUNK, N, wide_states);
+            stage.load(B + tp * c.ld_b, c.ld_b, C + tp * c.ld_c, c.ld_c, SEL_CHUNK, N, ok.bc);
         }
         cp_wait_all();
         __syncthreads();
 
-        // step size of row r; tokens past the end, and threads without a channel, take steps
-        // of nothing (their rows of the tiles were never written)
+        // Row r of a tile for this thread's channels.  Tokens past the end, and channels
+        // that the thread has not got (whose places were never written), read as zero.
+        auto two = [&](T(*tile)[CH], int r) {
+            const float2 v = reinterpret_cast<const Two<T> *>(&tile[r][ch])->f();
+            return make_float2(r < n && me.has > 0 ? v.x : 0.f, r < n && me.has > 1 ? v.y : 0.f);
+        };
         auto step_of = [&](int r) {
-            const float v = ld_f32<T>(&sh.dt[r][tid]) + bias;
-            const float s = c.softplus ? softplus_f(v) : v;
-            return r < n && me.in ? s : 0.f;
+            const float2 v = add2(two(sh.dt, r), bias), s = c.softplus ? softplus2(v) : v;
+            return make_float2(r < n && me.has > 0 ? s.x : 0.f, r < n && me.has > 1 ? s.y : 0.f);
+        };
+        // v[j], which every lane has for its own tokens, to all lanes of the pair: w[token]
+        auto spread = [&](const float2 (&v)[OWN], float2 (&w)[SUB]) {
+#pragma unroll
+            for (int k = 0; k < SUB; ++k) w[k] = SPLIT == 1 ? v[k / SPLIT] : shfl2(v[k / SPLIT], pair + k % SPLIT * PAIRS);
+        };
+        float2 dl[SUB], u2[SUB], own_dl[OWN], own[OWN];
+        auto steps_of_half = [&](int k0) {
+#pragma unroll
+            for (int j = 0; j < OWN; ++j) {
+                const int r = k0 + j * SPLIT + part;
+                own_dl[j] = step_of(r);
+                own[j] = mul2(own_dl[j], two(sh.x, r));
+            }
+            spread(own_dl, dl);
+            spread(own, u2);
         };
         if (n > SUB) {  // the state before the second half
-            float2 dl[SUB], u2[SUB];
-#pragma unroll
-            for (int k = 0; k < SUB; ++k) {
-                const float s = step_of(k);
-                dl[k] = splat(s), u2[k] = splat(me.in ? s * ld_f32<T>(&sh.x[k][tid]) : 0.f);
-            }
+            steps_of_half(0);
 #pragma unroll 2
-            for (int p = 0; p < P; ++p) {
-                const float2 A2 = sh.A2[p][tid];
-                float2 h = make_float2(sh.h0[2 * p][tid], sh.h0[2 * p + 1][tid]);
+            for (int s = 0; s < NS; ++s) {
+                const float2 A2 = sh.A2[s][tid];
+                float2 h = sh.h0[s][tid];
 #pragma unroll
                 for (int k = 0; k < SUB; ++k) {
-                    const float2 b = *reinterpret_cast<const float2 *>(sh.bc + k * P + p), arg = mul2(dl[k], A2);
+                    const float2 b = *reinterpret_cast<const float2 *>(sh.bc + k * NP + n0 + s), arg = mul2(dl[k], A2);
                     h = fma2(make_float2(ex2a(arg.x), ex2a(arg.y)), h, mul2(u2[k], b));
                 }
-                sh.hm[p][tid] = h;
+                sh.hm[s][tid] = h;
             }
         }
         for (int half = n > SUB ? 1 : 0; half >= 0; --half) {
             const int k0 = half * SUB;
-            float2 dl[SUB], u2[SUB], dp[SUB], du[SUB], sd[SUB], pre[SUB];
+            float2 dp[SUB], du[SUB], sd[SUB], pre[SUB];
+            steps_of_half(k0);
 #pragma unroll
-            for (int k = 0; k < SUB; ++k) {
-                const bool in = k0 + k < n && me.in;
-                const float s = step_of(k0 + k);
-                float e = ld_f32<T>(&sh.dy[k0 + k][tid]);
-                if (c.z) e *= silu_v(ld_f32<T>(&sh.z[k0 + k][tid]));
-                dl[k] = splat(s), u2[k] = splat(in ? s * ld_f32<T>(&sh.x[k0 + k][tid]) : 0.f), dp[k] = splat(in ? e : 0.f);
-                du[k] = sd[k] = pre[k] = make_float2(0.f, 0.f);
+            for (int j = 0; j < OWN; ++j) {
+                const int r = k0 + j * SPLIT + part;
+                own[j] = two(sh.dy, r);
+                if (c.z) own[j] = mul2(own[j], silu2(two(sh.z, r)));
             }
+            spread(own, dp);
+#pragma unroll
+            for (int k = 0; k < SUB; ++k) du[k] = sd[k] = pre[k] = zero;
+            const float2(*const h_from)[SCAN_THREADS] = half ? sh.hm : sh.h0;
 #pragma unroll 1
-            for (int p = 0; p < P; ++p) {
-                const float2 A2 = sh.A2[p][tid];
-                float2 h = half ? sh.hm[p][tid] : make_float2(sh.h0[2 * p][tid], sh.h0[2 * p + 1][tid]);
-                float2 a[SUB], hp[SUB], v[SUB];
-                const float4 *q = sh.bc + k0 * P + p;
+            for (int s2 = 0; s2 < NS; s2 += 2) {
+                ChannelSum<T, SPLIT> sums;
+                sums.clear();
 #pragma unroll
-                for (int k = 0; k < SUB; ++k) {
-                    const float4 bc = q[k * P];
-                    const float2 arg = mul2(dl[k], A2);
-                    a[k] = make_float2(ex2a(arg.x), ex2a(arg.y));
-                    hp[k] = h;
-                    h = fma2(a[k], h, mul2(u2[k], make_float2(bc.x, bc.y)));
-                    pre[k] = fma2(make_float2(bc.z, bc.w), h, pre[k]);
-                    v[k] = mul2(dp[k], h);
-                }
-                const float sC = channel_sum(v, lane);
-                float2 G = sh.G[p][tid], dA = sh.dA[p][tid];
+                for (int s = s2; s < s2 + 2; ++s) {
+                    const float2 A2 = sh.A2[s][tid];
+                    float2 h = h_from[s][tid], a[SUB], hp[SUB];
+                    float v[SUB];
+                    const float4 *q = sh.bc + k0 * NP + n0 + s;
 #pragma unroll
-                for (int k = SUB - 1; k >= 0; --k) {
-                    const float4 bc = q[k * P];
-                    const float2 g = fma2(dp[k], make_float2(bc.z, bc.w), G);
-                    G = mul2(a[k], g);
-                    const float2 qq = mul2(G, hp[k]);
-                    du[k] = fma2(g, make_float2(bc.x, bc.y), du[k]);
-                    sd[k] = fma2(A2, qq, sd[k]);
-                    dA = fma2(dl[k], qq, dA);
-                    v[k] = mul2(u2[k], g);
+                    for (int k = 0; k < SUB; ++k) {
+                        const float4 bc = q[k * NP];
+                        const float2 arg = mul2(dl[k], A2);
+                        a[k] = make_float2(ex2a(arg.x), ex2a(arg.y));
+                        hp[k] = h;
+                        h = fma2(a[k], h, mul2(u2[k], make_float2(bc.x, bc.y)));
+                        pre[k] = fma2(make_float2(bc.z, bc.w), h, pre[k]);
+                        const float2 e = mul2(dp[k], h);
+                        v[k] = e.x + e.y;
+                    }
+                    sums.add(v, 2 * (s - s2) + 1, lane);
+                    float2 G = sh.G[s][tid], dA = sh.dA[s][tid];
+#pragma unroll
+                    for (int k = SUB - 1; k >= 0; --k) {
+                        const float4 bc = q[k * NP];
+                        const float2 g = fma2(dp[k], make_float2(bc.z, bc.w), G);
+                        G = mul2(a[k], g);
+                        const float2 qq = mul2(G, hp[k]);
+                        du[k] = fma2(g, make_float2(bc.x, bc.y), du[k]);
+                        sd[k] = fma2(A2, qq, sd[k]);
+                        dA = fma2(dl[k], qq, dA);
+                        const float2 e = mul2(u2[k], g);
+                        v[k] = e.x + e.y;
+                    }
+                    sh.G[s][tid] = G, sh.dA[s][tid] = dA;
+                    sums.add(v, 2 * (s - s2), lane);
                 }
-                sh.G[p][tid] = G, sh.dA[p][tid] = dA;
-                const float sB = channel_sum(v, lane);
-                if ((lane & 3) < 2) {  // value lane/4 (+ 8): token value/2, state 2 p + value%2
-                    const int value = (lane >> 2) + 8 * (lane & 1);
-                    float *o = &sh.part[warp][value >> 1][0][2 * p + (value & 1)];
-                    o[0] = sB, o[NP] = sC;
-                }
+                const int which = lane & 1, state = n0 + s2 + ((lane >> 1) & 1);  // what instruction lane%4 summed
+                sums.finish(lane, [&](int token, float sum) { sh.part[warp][token][which][state] = sum; });
             }
+            sum_parts<SPLIT>(du, part);
+            sum_parts<SPLIT>(sd, part);
+            if (c.z) sum_parts<SPLIT>(pre, part);
 #pragma unroll
-            for (int k = 0; k < SUB; ++k) {
-                const int r = k0 + k;
-                const bool in = r < n && me.in;
-                const float xv = ld_f32<T>(&sh.x[r][tid]), duk = du[k].x + du[k].y;
-                float ddt = fmaf(xv, duk, (sd[k].x + sd[k].y) * 0.6931471805599453f);  // A was scaled by log2 e
-                if (c.softplus) ddt *= sigmoid_f(ld_f32<T>(&sh.dt[r][tid]) + bias);
-                const size_t o = (size_t)(t0 + r) * c.channels + d;
-                if (in) {
-                    st_f32<T>(static_cast<T *>(c.dx) + o, fmaf(dl[k].x, duk, Dv * dp[k].x));
-                    st_f32<T>(static_cast<T *>(c.ddt) + o, ddt);
-                    dD = fmaf(dp[k].x, xv, dD);
-                    dbias += ddt;
+            for (int j = 0; j < OWN; ++j) {
+                const int r = k0 + j * SPLIT + part;
+                const float2 xv = two(sh.x, r), dyv = two(sh.dy, r), e = own[j];
+                float2 ddt = fma2(xv, du[j], mul2(sd[j], splat(0.6931471805599453f)));  // A was scaled by log2 e
+                if (c.softplus) ddt = mul2(ddt, sigmoid2(add2(two(sh.dt, r), bias)));
+                if (r < n) {
+                    const size_t o = (size_t)(t0 + r) * c.channels;
+                    store_two<T>(static_cast<T *>(c.dx) + o, fma2(own_dl[j], du[j], mul2(D, e)), me, ok.paired);
+                    store_two<T>(static_cast<T *>(c.ddt) + o, ddt, me, ok.paired);
+                    dD = fma2(e, xv, dD);
+                    dbias = add2(dbias, ddt);
                     if (c.z) {
-                        const float zv = ld_f32<T>(&sh.z[r][tid]), s = sigmoid_f(zv), p = fmaf(Dv, xv, pre[k].x + pre[k].y);
-                        st_f32<T>(static_cast<T *>(c.dz) + o, ld_f32<T>(&sh.dy[r][tid]) * p * s * fmaf(zv, 1.f - s, 1.f));
+                        const float2 zv = two(sh.z, r), s = sigmoid2(zv), p = fma2(D, xv, pre[j]);
+                        const float2 one = splat(1.f), slope = mul2(s, fma2(zv, fma2(s, splat(-1.f), one), one));  // silu'
+                        store_two<T>(static_cast<T *>(c.dz) + o, mul2(mul2(dyv, p), slope), me, ok.paired);
                     }
                 }
             }
             __syncthreads();  // every warp's sums are there
-            for (int u = tid; u < SUB * 2 * NP; u += THREADS) {
+            for (int u = tid; u < SUB * 2 * NP; u += SCAN_THREADS) {
                 const int t = u / (2 * NP), k = u % (2 * NP), s = k % NP;
                 float v = (&sh.part[0][0][0][0])[u];
 #pragma unroll
@@ -277,72 +296,80 @@ __global__ void __launch_bounds__(bwd_threads<NP>(), NP <= 16 ? 3 : 1) sel_bwd_k
             __syncthreads();  // before the other half's
         }
     }
-    if (!me.in) return;
-    for (int s = 0; s < N; ++s) pa[(size_t)s * c.channels] = s & 1 ? sh.dA[s / 2][tid].y : sh.dA[s / 2][tid].x;
-    pd_[0] = dD;
-    pd_[c.channels] = dbias;
+    for (int k = 0; k < NS; ++k)
+        if (n0 + k < N) store_two<float>(pa + (size_t)(n0 + k) * c.channels, sh.dA[k][tid], me, ok.state);
+#pragma unroll
+    for (int o = PAIRS; o < 32; o *= 2) {
+        dD = add2(dD, make_float2(__shfl_xor_sync(0xffffffffu, dD.x, o), __shfl_xor_sync(0xffffffffu, dD.y, o)));
+        dbias = add2(dbias, make_float2(__shfl_xor_sync(0xffffffffu, dbias.x, o), __shfl_xor_sync(0xffffffffu, dbias.y, o)));
+    }
+    if (part == 0) store_two<float>(pdd, dD, me, ok.state), store_two<float>(pdd + c.channels, dbias, me, ok.state);
 }
 
 // What a segment hands back when nothing comes from behind it, and its sum of steps: for
 // sel_join.  The first segment of a sequence hands back to nobody.
-constexpr int CARRY_THREADS = 64;
 template <typename T, int NP>
-__global__ void __launch_bounds__(CARRY_THREADS) sel_carry_kernel(SelCall c, Segments sg, bool wide) {
-    constexpr int P = NP / 2;
-    using Stage = StageBC<T, NP, SEL_CHUNK, CARRY_THREADS>;
-    __shared__ __align__(16) float4 bc[Stage::BYTES / 16];
+__global__ void __launch_bounds__(SCAN_THREADS) sel_carry_kernel(SelCall c, Segments sg, Access ok) {
+    using L = Lanes<NP>;
+    constexpr int NS = L::NS, SPLIT = L::SPLIT, PAIRS = L::PAIRS, OWN = GROUP / SPLIT;
+    using Stage = StageBC<T, NP, SEL_CHUNK, true>;
+    __shared__ __align__(16) float4 bc[SEL_CHUNK * NP];
     int i, first, lo, hi, end;
     if (!segment(c.seq, sg.seg, blockIdx.x, i, first, lo, hi, end) || lo == first) return;
-    const Mine me = my_channel<CARRY_THREADS>(c, blockIdx.y);
-    const int N = c.dstate, d = me.channel;
+    const Mine me = my_channels<NP>(c, blockIdx.y);
+    const int N = c.dstate, lane = threadIdx.x & 31, part = lane / PAIRS, pair = lane % PAIRS, n0 = part * NS;
     const T *B = static_cast<const T *>(c.B) + me.group * N, *C = static_cast<const T *>(c.C) + me.group * N;
-    const T *dt = static_cast<const T *>(c.dt) + d, *z = static_cast<const T *>(c.z) + (c.z ? d : 0), *dy = static_cast<const T *>(c.dy) + d;
-    float2 A2[P], R[P];
+    const T *dt = static_cast<const T *>(c.dt), *z = static_cast<const T *>(c.z), *dy = static_cast<const T *>(c.dy);
+    float2 A2[NS], R[NS];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        A2[p] = make_float2(2 * p < N ? c.A[(size_t)d * N + 2 * p] * LOG2E : 0.f, 2 * p + 1 < N ? c.A[(size_t)d * N + 2 * p + 1] * LOG2E : 0.f);
-        R[p] = make_float2(0.f, 0.f);
+    for (int k = 0; k < NS; ++k) {
+        const int n = min(n0 + k, N - 1);
+        A2[k] = make_float2(c.A[(size_t)me.c0 * N + n] * LOG2E, c.A[(size_t)me.c1 * N + n] * LOG2E);
+        R[k] = make_float2(0.f, 0.f);
     }
-    const float bias = c.dt_bias ? c.dt_bias[d] : 0.f;
-    float steps = 0.f;
+    const float2 bias = c.dt_bias ? make_float2(c.dt_bias[me.c0], c.dt_bias[me.c1]) : make_float2(0.f, 0.f);
+    float2 steps = make_float2(0.f, 0.f);
     for (int t0 = lo + (hi - 1 - lo) / SEL_CHUNK * SEL_CHUNK; t0 >= lo; t0 -= SEL_CHUNK) {
         const int n = min(SEL_CHUNK, hi - t0);
         Stage stage;
-        stage.load(B + t0 * c.ld_b, c.ld_b, C + t0 * c.ld_c, c.ld_c, n, N, wide);
+        stage.load(B + t0 * c.ld_b, c.ld_b, C + t0 * c.ld_c, c.ld_c, n, N, ok.bc);
         __syncthreads();
         stage.put(bc);
         __syncthreads();
-        constexpr int G = 4;
 #pragma unroll 1
-        for (int t = (n - 1) / G * G; t >= 0; t -= G) {
-            float dl[G], e[G];
+        for (int t = (n - 1) / GROUP * GROUP; t >= 0; t -= GROUP) {
+            float2 dl[OWN], e[OWN];
 #pragma unroll
-            for (int k = 0; k < G; ++k) {
-                const int row = t0 + min(t + k, n - 1);
-                dl[k] = ld_f32<T>(dt + row * c.ld_dt) + bias, e[k] = ld_f32<T>(dy + (size_t)row * c.channels);
-                if (c.softplus) dl[k] = softplus_f(dl[k]);
-                if (c.z) e[k] *= silu_v(ld_f32<T>(z + row * c.ld_z));
+            for (int j = 0; j < OWN; ++j) {
+                const int at = t + j * SPLIT + part, row = t0 + min(at, n - 1);
+                dl[j] = add2(load_two(dt + row * c.ld_dt, me, ok.paired).f(), bias);
+                e[j] = load_two(dy + (size_t)row * c.channels, me, ok.paired).f();
+                if (c.softplus) dl[j] = softplus2(dl[j]);
+                if (c.z) e[j] = mul2(e[j], silu2(load_two(z + row * c.ld_z, me, ok.paired).f()));
+                if (at >= n) dl[j] = e[j] = make_float2(0.f, 0.f);
+                steps = add2(steps, dl[j]);
             }
 #pragma unroll
-            for (int k = G - 1; k >= 0; --k) {
-                if (t + k >= n) continue;
-                const float2 d2 = splat(dl[k]), e2 = splat(e[k]);
-                steps += dl[k];
+            for (int k = GROUP - 1; k >= 0; --k) {
+                const int from = pair + k % SPLIT * PAIRS;
+                const float2 d2 = SPLIT == 1 ? dl[k / SPLIT] : shfl2(dl[k / SPLIT], from), e2 = SPLIT == 1 ? e[k / SPLIT] : shfl2(e[k / SPLIT], from);
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    const float4 v = bc[(t + k) * P + p];
-                    const float2 arg = mul2(d2, A2[p]);
-                    R[p] = mul2(make_float2(ex2a(arg.x), ex2a(arg.y)), fma2(e2, make_float2(v.z, v.w), R[p]));
+                for (int s = 0; s < NS; ++s) {
+                    const float4 v = bc[(t + k) * NP + n0 + s];
+                    const float2 arg = mul2(d2, A2[s]);
+                    R[s] = mul2(make_float2(ex2a(arg.x), ex2a(arg.y)), fma2(e2, make_float2(v.z, v.w), R[s]));
                 }
             }
         }
     }
-    if (!me.in) return;
-    float *o = sg.state + (size_t)blockIdx.x * N * c.channels + d;
+    float *o = sg.state + (size_t)blockIdx.x * N * c.channels;
 #pragma unroll
-    for (int n = 0; n < NP; ++n)
-        if (n < N) o[(size_t)n * c.channels] = n & 1 ? R[n / 2].y : R[n / 2].x;
-    sg.steps[(size_t)blockIdx.x * c.channels + d] = steps;
+    for (int k = 0; k < NS; ++k)
+        if (n0 + k < N) store_two<float>(o + (size_t)(n0 + k) * c.channels, R[k], me, ok.state);
+#pragma unroll
+    for (int k = PAIRS; k < 32; k *= 2)
+        steps = add2(steps, make_float2(__shfl_xor_sync(0xffffffffu, steps.x, k), __shfl_xor_sync(0xffffffffu, steps.y, k)));
+    if (part == 0) store_two<float>(sg.steps + (size_t)blockIdx.x * c.channels, steps, me, ok.state);
 }
 
 // The sums over blocks.  The first row_blocks blocks: dB and dC, a warp per token,
@@ -402,8 +429,8 @@ struct Layout {  // of the workspace, in floats
     Layout(int tokens, int nseq, int channels, int groups, int N) {
         seg = choose_seg(tokens, nseq, channels, BWD_WARPS_PER_SM);
         slots = tokens > 0 ? seg_slots(tokens, nseq, seg) : 0;
-        const int threads = N <= 32 ? 128 : 64;
-        tiles = (channels / groups + threads - 1) / threads;
+        const int split = N <= 8 ? 1 : N <= 16 ? 2 : 4, ch = 2 * SCAN_THREADS / split;  // as Lanes
+        tiles = (channels / groups + ch - 1) / ch;
         bc = 0;
         a = bc + (size_t)groups * tiles * tokens * 2 * N;
         d = a + (size_t)slots * channels * N;
@@ -414,26 +441,23 @@ struct Layout {  // of the workspace, in floats
 };
 
 template <typename T> cudaError_t run(const SelCall &c, float *ws, cudaStream_t st) {
-    const size_t e = sizeof(T);
-    const int per_group = c.channels / c.groups;
     const Layout l(c.seq.tokens, c.seq.nseq, c.channels, c.groups, c.dstate);
-    const bool wide = rows_aligned(c.x, c.ld_x, e, 16) && rows_aligned(c.dt, c.ld_dt, e, 16) &&
-                      (!c.z || rows_aligned(c.z, c.ld_z, e, 16)) && c.channels * e % 16 == 0 && per_group * e % 16 == 0;
-    const bool wb = wide_bc(c);
     const Parts p{ws + l.bc, ws + l.a, ws + l.d};
     const Segments sg{l.seg, l.slots, ws + l.carried, ws + l.steps};
+    const Access ok(c);
     if (c.seq.nseq > 0 && c.seq.tokens > 0) {
         const cudaError_t err = with_states(c.dstate, [&](auto np) {
-            constexpr int TH = bwd_threads<np()>();
-            const size_t smem = sizeof(BwdShared<T, np()>);
-            cudaError_t r = cudaFuncSetAttribute(sel_bwd_kernel<T, np()>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            const dim3 grid(l.slots, channel_tiles<np()>(c));
+            constexpr size_t smem = sizeof(BwdShared<T, np()>);
+            cudaError_t r = cudaSuccess;
+            if (smem > 48 << 10) r = cudaFuncSetAttribute(sel_bwd_kernel<T, np()>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (r == cudaSuccess && l.seg != WHOLE) {
-                sel_carry_kernel<T, np()><<<dim3(l.slots, channel_tiles<CARRY_THREADS>(c)), CARRY_THREADS, 0, st>>>(c, sg, wb);
+                sel_carry_kernel<T, np()><<<grid, SCAN_THREADS, 0, st>>>(c, sg, ok);
                 r = cudaGetLastError();
                 if (r == cudaSuccess) r = launch_sel_join(c, sg, true, st);
             }
             if (r != cudaSuccess) return r;
-            sel_bwd_kernel<T, np()><<<dim3(l.slots, channel_tiles<TH>(c)), TH, smem, st>>>(c, sg, p, wide, wb);
+            sel_bwd_kernel<T, np()><<<grid, SCAN_THREADS, smem, st>>>(c, sg, p, ok);
             return cudaGetLastError();
         });
         if (err != cudaSuccess) return err;

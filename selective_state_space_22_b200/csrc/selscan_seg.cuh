@@ -1,8 +1,10 @@
 // selscan_seg.cuh -- what the forward and backward selective scans share: the cut of
 // sequences into segments, the staging of B and C, and the join of segments.
 //
-// A thread walks the recurrence of one channel, its states in registers two to a
-// float2, so that every operation but the exponential is a packed one.  Where the
+// A thread walks the recurrence of some states of a channel (backwards: of two channels),
+// two values in the halves of a float2, so that every operation but the exponential is a
+// packed one; the lanes that share a channel's states take turns at the work per channel
+// and token (step size, gate).  Where the
 // (sequence, channel) pairs do not fill the GPU, sequences are cut into segments of
 // `seg` tokens: a first pass runs every segment but a sequence's last from zero and
 // keeps its end state and its sum of steps, sel_join carries the states from segment
@@ -60,14 +62,53 @@ __device__ __forceinline__ bool segment(const Packed &p, int seg, int s, int &i,
     return true;
 }
 
-// B and C of TT tokens in shared memory: token t, states 2 p and 2 p + 1 as
-// (B, B, C, C), so that one 16-byte read, the same for all lanes, feeds a pair of
-// states.  Fetched a run ahead: `load` takes the rows into registers as they lie in
+// Backwards, how dstate (padded to NP) states are shared out: NS to a lane, SPLIT <= 4
+// lanes to a channel pair, lane = pair + PAIRS * part.  GROUP tokens are taken at a time, so that
+// each lane has a whole number of them to prepare.
+constexpr int GROUP = 4;
+template <int NP> struct Lanes {
+    static constexpr int NS = NP < 8 ? NP : NP <= 32 ? 8 : 16, SPLIT = NP / NS, PAIRS = 32 / SPLIT, CH = 64 / SPLIT;  // CH: channels of a warp
+};
+constexpr int SCAN_THREADS = 64;
+
+__device__ __forceinline__ void cp16(void *smem, const void *gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem)
+                 : "memory");
+}
+__device__ __forceinline__ void cp8(void *smem, const void *gmem) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp4(void *smem, const void *gmem) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// n rows of `cols` channels into tile[..][CH]; wide: aligned 16-byte pieces, which
+// land by cp_wait_all, else plain copies.
+template <typename T, int CH>
+__device__ __forceinline__ void fetch_rows(T (*to)[CH], const T *src, long long ld, int n, int cols, bool wide) {
+    constexpr int E = 16 / (int)sizeof(T), PER = CH / E;
+    if (wide) {
+        for (int u = threadIdx.x; u < n * PER; u += SCAN_THREADS) {
+            const int r = u / PER, k = u % PER * E;
+            if (k < cols) cp16(&to[r][k], src + r * ld + k);
+        }
+    } else {
+        for (int u = threadIdx.x; u < n * CH; u += SCAN_THREADS) {
+            const int r = u / CH, k = u % CH;
+            if (k < cols) to[r][k] = src[r * ld + k];
+        }
+    }
+}
+
+// B and C of TT tokens in shared memory, for 16-byte reads that are the same for all
+// lanes with those states: of token t, states 2 p and 2 p + 1 as (B, B', C, C'), or with
+// TWICE state n as (B, B, C, C) for two channels at once.
+// Fetched a run ahead: `load` takes the rows into registers as they lie in
 // memory, `put` writes them out once the buffer is free.  Tokens past the run's end and
 // states past N are zero.
-template <typename T, int NP, int TT, int THREADS> struct StageBC {
-    static constexpr int QUADS = TT * NP / 4, PER = (QUADS + THREADS - 1) / THREADS;  // of B, and of C
-    static constexpr int BYTES = TT * NP * 8;
+template <typename T, int NP, int TT, bool TWICE> struct StageBC {
+    static constexpr int QUADS = TT * NP / 4, PER = (QUADS + SCAN_THREADS - 1) / SCAN_THREADS;  // of B, and of C
     struct alignas(4 * sizeof(T)) Quad {
         T v[4];
     };
@@ -86,7 +127,7 @@ template <typename T, int NP, int TT, int THREADS> struct StageBC {
     __device__ __forceinline__ void load(const T *B, long long lb, const T *C, long long lc, int n, int N, bool wide) {
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
-            const int at = u * THREADS + threadIdx.x, t = at / (NP / 4), s = at % (NP / 4) * 4;
+            const int at = u * SCAN_THREADS + threadIdx.x, t = at / (NP / 4), s = at % (NP / 4) * 4;
             const int left = t < n && at < QUADS ? N - s : 0;
             b[u] = get(B + (left > 0 ? t * lb + s : 0), left, wide);
             c[u] = get(C + (left > 0 ? t * lc + s : 0), left, wide);
@@ -95,36 +136,97 @@ template <typename T, int NP, int TT, int THREADS> struct StageBC {
     __device__ __forceinline__ void put(float4 *to) const {
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
-            const int at = u * THREADS + threadIdx.x;
+            const int at = u * SCAN_THREADS + threadIdx.x;
             if (at >= QUADS) break;
             float fb[4], fc[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) fb[i] = ld_f32<T>(&b[u].v[i]), fc[i] = ld_f32<T>(&c[u].v[i]);
-            to[2 * at] = make_float4(fb[0], fb[1], fc[0], fc[1]);
-            to[2 * at + 1] = make_float4(fb[2], fb[3], fc[2], fc[3]);
+            if constexpr (TWICE) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to[4 * at + i] = make_float4(fb[i], fb[i], fc[i], fc[i]);
+            } else {
+                to[2 * at] = make_float4(fb[0], fb[1], fc[0], fc[1]);
+                to[2 * at + 1] = make_float4(fb[2], fb[3], fc[2], fc[3]);
+            }
         }
     }
 };
 
-// Channels of block `tile` of THREADS: first channel, group, and whether this thread has one.
+// A thread's channel pair: its first channel, the second (the first again where the
+// group ends), and how many of the two it has (0 to 2).
 struct Mine {
-    int group, channel;
-    bool in;
+    int group, c0, c1, has;
 };
-template <int THREADS> __device__ __forceinline__ Mine my_channel(const SelCall &c, int tile) {
-    const int per_group = c.channels / c.groups, tiles = (per_group + THREADS - 1) / THREADS;
-    const int g = tile / tiles, k = tile % tiles * THREADS + threadIdx.x;
-    return {g, g * per_group + min(k, per_group - 1), k < per_group};
+template <int NP> __device__ __forceinline__ Mine my_channels(const SelCall &c, int tile) {
+    using L = Lanes<NP>;
+    constexpr int CH = SCAN_THREADS / 32 * L::CH;  // channels of a block
+    const int per_group = c.channels / c.groups, tiles = (per_group + CH - 1) / CH, g = tile / tiles;
+    const int k = tile % tiles * CH + 2 * ((threadIdx.x >> 5) * L::PAIRS + (threadIdx.x & 31) % L::PAIRS);
+    const int first = min(k, (per_group - 1) & ~1);  // threads past the group follow along on its last pair
+    return {g, g * per_group + first, g * per_group + min(first + 1, per_group - 1), max(0, min(2, per_group - k))};
 }
-template <int THREADS> inline int channel_tiles(const SelCall &c) {
-    return c.groups * ((c.channels / c.groups + THREADS - 1) / THREADS);
+template <int NP> inline int channel_tiles(const SelCall &c) {
+    constexpr int CH = SCAN_THREADS / 32 * Lanes<NP>::CH;
+    return c.groups * ((c.channels / c.groups + CH - 1) / CH);
 }
 
-inline bool wide_bc(const SelCall &c) {
+// Two neighbouring values of a row.  paired: one aligned access.
+template <typename T> struct alignas(2 * sizeof(T)) Two {
+    T a, b;
+    __device__ __forceinline__ float2 f() const { return make_float2(ld_f32<T>(&a), ld_f32<T>(&b)); }
+};
+template <typename T> __device__ __forceinline__ Two<T> load_two(const T *row, const Mine &me, bool paired) {
+    if (paired) return *reinterpret_cast<const Two<T> *>(row + me.c0);
+    return {row[me.c0], row[me.c1]};
+}
+template <typename T> __device__ __forceinline__ void store_two(T *row, float2 v, const Mine &me, bool paired) {
+    Two<T> t;
+    st_f32<T>(&t.a, v.x), st_f32<T>(&t.b, v.y);
+    if (paired) {
+        if (me.has) *reinterpret_cast<Two<T> *>(row + me.c0) = t;
+    } else {
+        if (me.has > 0) row[me.c0] = t.a;
+        if (me.has > 1) row[me.c1] = t.b;
+    }
+}
+__device__ __forceinline__ float2 shfl2(float2 v, int lane) {
+    return make_float2(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane));
+}
+// v[k] summed over the SPLIT lanes of a channel pair: a lane of part s ends with token
+// j SPLIT + s in v[j].
+template <int SPLIT, int K> __device__ __forceinline__ void sum_parts(float2 (&v)[K], int part) {
+    constexpr int PAIRS = 32 / SPLIT;
+#pragma unroll
+    for (int j = 0; j < K / SPLIT; ++j) {
+        float2 t[SPLIT];
+#pragma unroll
+        for (int u = 0; u < SPLIT; ++u) t[u] = v[j * SPLIT + u];
+#pragma unroll
+        for (int n = SPLIT / 2; n > 0; n /= 2)
+#pragma unroll
+            for (int u = 0; u < n; ++u) {
+                const float2 keep = part & n ? t[u + n] : t[u], give = part & n ? t[u] : t[u + n];
+                t[u] = add2(keep, make_float2(__shfl_xor_sync(0xffffffffu, give.x, n * PAIRS), __shfl_xor_sync(0xffffffffu, give.y, n * PAIRS)));
+            }
+        v[j] = t[0];
+    }
+}
+
+// Whether every row of x, dt and z (and with them y and the gradients, which are
+// contiguous) divides into aligned pieces of so many bytes from each group's start on.
+inline bool rows_in(const SelCall &c, size_t bytes) {
     const size_t e = c.bf16 ? 2 : 4;
-    return c.dstate % 4 == 0 && rows_aligned(c.B, c.ld_b, e, 4 * e) && rows_aligned(c.C, c.ld_c, e, 4 * e);
+    return c.channels / c.groups * e % bytes == 0 && rows_aligned(c.x, c.ld_x, e, bytes) && rows_aligned(c.dt, c.ld_dt, e, bytes) &&
+           (!c.z || rows_aligned(c.z, c.ld_z, e, bytes));
 }
-
+struct Access {
+    bool wide, paired, state, bc;  // 16-byte pieces of rows, pairs of channels, pairs of float32, quads of B and C
+    explicit Access(const SelCall &c) {
+        const size_t e = c.bf16 ? 2 : 4;
+        wide = rows_in(c, 16), paired = rows_in(c, 2 * e), state = c.channels / c.groups % 2 == 0;
+        bc = c.dstate % 4 == 0 && rows_aligned(c.B, c.ld_b, e, 4 * e) && rows_aligned(c.C, c.ld_c, e, 4 * e);
+    }
+};
 // The states that segments start from, in place of the ones they end with from zero:
 // forwards h_{j+1} = exp(A steps_j) h_j + S_j from the sequence's initial state,
 // backwards the same from the last segment, from zero.

@@ -115,7 +115,7 @@ def test_scan_refusals_of_each_call(lib):
     assert varlen(n=1 << 20, ws=None) == WORK and varlen(n=1 << 20) == WORK and varlen(ws=OFF) == BAD
     assert lib.ssd_selective_scan_workspace_size(1 << 20, 2, 64, 16) > 1 << 20
     assert lib.ssd_selective_scan_workspace_size(64 * 512, 64, 1024, 16) == 0
-    assert lib.ssd_selective_scan_chunk_states(300, 3) == 300 // 16 + 3 and lib.ssd_selective_scan_chunk_states(-1, 3) == ssd.SSD_WORKSPACE_INVALID
+    assert lib.ssd_selective_scan_chunk_states(300, 3) == 300 // 8 + 3 and lib.ssd_selective_scan_chunk_states(-1, 3) == ssd.SSD_WORKSPACE_INVALID
     assert lib.ssd_selective_scan_bwd_workspace_size(10, 2, 64, 3, 16) == ssd.SSD_WORKSPACE_INVALID
 
 
