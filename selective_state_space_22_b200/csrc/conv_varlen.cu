@@ -492,20 +492,23 @@ __global__ void __launch_bounds__(32 * WARPS, V == 2 ? 5 : 4) conv_bwd_kernel(co
         }
 }
 
-// dw[c][k] and dbias[c] from the blocks' parts [parts][channels][K+1]: 32 lanes
-// take every 32nd part, then a butterfly.
-__global__ void __launch_bounds__(256) conv_bwd_sum(const float *__restrict__ part, int parts, int channels, int K,
-                                                   float *__restrict__ dw, float *__restrict__ db) {
-    __shared__ float s[8][33];
-    const int o = blockIdx.x * 32 + (threadIdx.x & 31), q = threadIdx.x >> 5, n = channels * (K + 1);
+// dw[c][k] and dbias[c] from the blocks' parts [parts][channels][K+1]: 32 warps take
+// every 32nd.
+__global__ void __launch_bounds__(1024) conv_bwd_sum(const float *__restrict__ part, int parts, int channels, int K,
+                                                    float *__restrict__ dw, float *__restrict__ db) {
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5, n = channels * (K + 1), at = blockIdx.x * 32 + lane;
     float a = 0.f;
-    if (o < n)
-        for (int i = q; i < parts; i += 8) a += part[(size_t)i * n + o];
-    s[q][threadIdx.x & 31] = a;
+    if (at < n)
+#pragma unroll 4
+        for (int i = q; i < parts; i += 32) a += part[(size_t)i * n + at];
+    s[q][lane] = a;
     __syncthreads();
-    if (q || o >= n) return;
-    for (int i = 1; i < 8; ++i) a += s[i][threadIdx.x];
-    const int c = o / (K + 1), k = o % (K + 1);
+    a = s[lane][q];  // element q of the block
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    const int e = blockIdx.x * 32 + q, c = e / (K + 1), k = e % (K + 1);
+    if (lane || e >= n) return;
     if (k < K)
         dw[(size_t)c * K + k] = a;
     else if (db)
@@ -543,7 +546,7 @@ template <typename T, int V, int KT, bool EXACT> cudaError_t run_bwd(const ConvC
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    conv_bwd_sum<<<(ctot * (c.width + 1) + 31) / 32, 256, 0, st>>>(ws, parts, ctot, c.width, c.dw, c.db);
+    conv_bwd_sum<<<(ctot * (c.width + 1) + 31) / 32, 1024, 0, st>>>(ws, parts, ctot, c.width, c.dw, c.db);
     return cudaGetLastError();
 }
 template <typename T, int V> cudaError_t pick_bwd(const ConvCall &c, float *ws, cudaStream_t st) {

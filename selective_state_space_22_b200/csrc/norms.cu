@@ -22,7 +22,8 @@
 namespace ssd {
 namespace {
 
-constexpr int BWD_BLOCKS = 592;  // 4 blocks of 256 threads per SM on 148 SMs
+constexpr int BWD_BLOCKS = 296;   // of 256 threads: the two per SM that fit their registers, on 148 SMs
+constexpr int MANY_UNITS = 2368;  // 16 per SM
 
 // Sums of (a, b) over the TPR threads of a unit; every thread of the block calls it.
 template <int TPR> __device__ __forceinline__ float2 unit_sum(float2 v, float2 *sh) {
@@ -182,6 +183,17 @@ __device__ __forceinline__ void put_parts(const float (&dw)[VPT][V], const float
     }
 }
 
+// V channels of a row as they lie in memory: the next row's are on their way while this
+// one is worked on (without, the gradients took 109 us where they take BEFORE_TIME and
+// AFTER_OLD us where they take AFTER_TIME: 16384 x 2048 and 8192 x 8 x 512 channels).
+template <typename T, int V> struct alignas(V * sizeof(T) < 16 ? V * sizeof(T) : 16) Raw {
+    T v[V];
+    __device__ __forceinline__ void get(float (&f)[V]) const { load_v<T, V, (V > 1)>(v, f); }
+};
+template <typename T, int V> __device__ __forceinline__ Raw<T, V> raw_at(const void *p, size_t at) {
+    return *reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(p) + at);
+}
+
 template <typename T, typename TR, int V, int VPT, int TPR>
 __global__ void __launch_bounds__(block_threads<TPR>()) norm_before_bwd_kernel(NormCall c, float *part) {
     constexpr bool WIDE = V > 1;
@@ -197,10 +209,27 @@ __global__ void __launch_bounds__(block_threads<TPR>()) norm_before_bwd_kernel(N
         for (int v = 0; v < V; ++v) dw[q][v] = ds[q][v] = w[q][v] = 0.f;
         if (k < c.width) load_v<float, V, WIDE>(c.w + k, w[q]);
     }
+    Raw<TR, V> nr[VPT], nu[VPT];  // r and its upstream gradient
+    Raw<T, V> nd[VPT], nx[VPT];   // dout and x
+    auto fetch = [&](int row) {
+        if (row >= c.rows) return;
+#pragma unroll
+        for (int q = 0; q < VPT; ++q) {
+            const int k = (q * TPR + t) * V;
+            if (k >= c.width) continue;
+            nr[q] = raw_at<TR, V>(c.res, row * c.ld_res + k);
+            nd[q] = raw_at<T, V>(c.dout, (size_t)row * c.width + k);
+            if (c.dres) nu[q] = raw_at<TR, V>(c.dres, (size_t)row * c.width + k);
+            if (c.scale) nx[q] = raw_at<T, V>(c.x, row * c.ld_x + k);
+        }
+    };
+    fetch(blockIdx.x * U + unit);
     for (int row0 = blockIdx.x * U; row0 < c.rows; row0 += gridDim.x * U) {
         const int row = row0 + unit;
         const bool in = row < c.rows;
         float r[VPT][V], d[VPT][V];
+        Raw<TR, V> cu[VPT];
+        Raw<T, V> cx[VPT];
         float2 s = make_float2(0.f, 0.f);
 #pragma unroll
         for (int q = 0; q < VPT; ++q) {
@@ -208,14 +237,16 @@ __global__ void __launch_bounds__(block_threads<TPR>()) norm_before_bwd_kernel(N
 #pragma unroll
             for (int v = 0; v < V; ++v) r[q][v] = d[q][v] = 0.f;
             if (!in || k >= c.width) continue;
-            load_v<TR, V, WIDE>(static_cast<const TR *>(c.res) + row * c.ld_res + k, r[q]);
-            load_v<T, V, WIDE>(static_cast<const T *>(c.dout) + (size_t)row * c.width + k, d[q]);
+            nr[q].get(r[q]);
+            nd[q].get(d[q]);
+            cu[q] = nu[q], cx[q] = nx[q];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 s.x = fmaf(r[q][v], r[q][v], s.x);
                 s.y = fmaf(d[q][v] * w[q][v], r[q][v], s.y);
             }
         }
+        fetch(row + gridDim.x * U);
         s = unit_sum<TPR>(s, sh);
         const float rstd = 1.f / sqrtf(s.x / c.width + c.eps), m = s.y * rstd / c.width;
 #pragma unroll
@@ -230,13 +261,13 @@ __global__ void __launch_bounds__(block_threads<TPR>()) norm_before_bwd_kernel(N
                 d[q][v] = rstd * (d[q][v] * w[q][v] - n * m);
             }
             if (c.dres) {
-                load_v<TR, V, WIDE>(static_cast<const TR *>(c.dres) + (size_t)row * c.width + k, a);
+                cu[q].get(a);
 #pragma unroll
                 for (int v = 0; v < V; ++v) d[q][v] += a[v];
             }
             if (c.dres_out) store_v<TR, V, WIDE>(static_cast<TR *>(c.dres_out) + (size_t)row * c.width + k, d[q]);
             if (c.scale) {
-                load_v<T, V, WIDE>(static_cast<const T *>(c.x) + row * c.ld_x + k, a);
+                cx[q].get(a);
 #pragma unroll
                 for (int v = 0; v < V; ++v) ds[q][v] = fmaf(d[q][v], a[v], ds[q][v]);
                 load_v<float, V, WIDE>(c.scale + k, a);
@@ -249,7 +280,10 @@ __global__ void __launch_bounds__(block_threads<TPR>()) norm_before_bwd_kernel(N
     put_parts<V, VPT, TPR>(dw, ds, c.scale != nullptr, 0, c.width, c.width, part, sums);
 }
 
-template <typename T, int V, int VPT, int TPR>
+// FIRST: the norm before the gate.  What is there or not (gate, scale) is asked once per
+// vector, not per channel: with the questions inside, a channel took 67 instructions and
+// the kernel 90 us where it takes AFTER_TIME.
+template <typename T, int V, int VPT, int TPR, bool FIRST>
 __global__ void __launch_bounds__(block_threads<TPR>()) norm_after_bwd_kernel(NormCall c, float *part) {
     constexpr bool WIDE = V > 1;
     constexpr int U = block_threads<TPR>() / TPR;
@@ -265,52 +299,81 @@ __global__ void __launch_bounds__(block_threads<TPR>()) norm_after_bwd_kernel(No
         for (int v = 0; v < V; ++v) dw[q][v] = ds[q][v] = w[q][v] = 0.f;
         if (k < gw) load_v<float, V, WIDE>(c.w + g0 + k, w[q]);
     }
+    Raw<T, V> ny[VPT], nz[VPT], nd[VPT];
+    auto fetch = [&](int row) {
+        if (row >= c.rows) return;
+#pragma unroll
+        for (int q = 0; q < VPT; ++q) {
+            const int k = (q * TPR + t) * V;
+            if (k >= gw) continue;
+            ny[q] = raw_at<T, V>(c.x, row * c.ld_x + g0 + k);
+            if (c.z) nz[q] = raw_at<T, V>(c.z, row * c.ld_z + g0 + k);
+            nd[q] = raw_at<T, V>(c.dout, (size_t)row * c.width + g0 + k);
+        }
+    };
+    fetch(blockIdx.x * U + unit);
     for (int row0 = blockIdx.x * U; row0 < c.rows; row0 += gridDim.x * U) {
         const int row = row0 + unit;
         const bool in = row < c.rows;
-        float y[VPT][V], z[VPT][V], d[VPT][V];
+        float y[VPT][V], gate[VPT][V], sg[VPT][V], d[VPT][V];  // d: the gradient at the norm's (gated) result
+        Raw<T, V> cd[VPT];
         float2 s = make_float2(0.f, 0.f);
 #pragma unroll
         for (int q = 0; q < VPT; ++q) {
             const int k = (q * TPR + t) * V;
 #pragma unroll
-            for (int v = 0; v < V; ++v) y[q][v] = z[q][v] = d[q][v] = 0.f;
+            for (int v = 0; v < V; ++v) y[q][v] = d[q][v] = 0.f, gate[q][v] = sg[q][v] = 1.f;
             if (!in || k >= gw) continue;
-            load_v<T, V, WIDE>(static_cast<const T *>(c.x) + row * c.ld_x + g0 + k, y[q]);
-            if (c.z) load_v<T, V, WIDE>(static_cast<const T *>(c.z) + row * c.ld_z + g0 + k, z[q]);
-            load_v<T, V, WIDE>(static_cast<const T *>(c.dout) + (size_t)row * c.width + g0 + k, d[q]);
-            float a[V];
-            if (c.scale) load_v<float, V, WIDE>(c.scale + g0 + k, a);
+            ny[q].get(y[q]);
+            nd[q].get(d[q]);
+            cd[q] = nd[q];
+            if (c.z) {
+                nz[q].get(gate[q]);
+#pragma unroll
+                for (int v = 0; v < V; ++v) sg[q][v] = sigmoid_f(gate[q][v]), gate[q][v] *= sg[q][v];
+            }
+            if (c.scale) {
+                float a[V];
+                load_v<float, V, WIDE>(c.scale + g0 + k, a);
+#pragma unroll
+                for (int v = 0; v < V; ++v) d[q][v] *= a[v];
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float gate = c.z ? silu_v(z[q][v]) : 1.f;
-                const float vv = c.norm_first ? y[q][v] : y[q][v] * gate;
-                const float dn = d[q][v] * (c.scale ? a[v] : 1.f) * (c.norm_first ? gate : 1.f) * w[q][v];
+                const float vv = FIRST ? y[q][v] : y[q][v] * gate[q][v], dm = FIRST ? d[q][v] * gate[q][v] : d[q][v];
                 s.x = fmaf(vv, vv, s.x);
-                s.y = fmaf(dn, vv, s.y);
+                s.y = fmaf(dm * w[q][v], vv, s.y);
             }
         }
+        fetch(row + gridDim.x * U);
         s = unit_sum<TPR>(s, sh);
         const float rstd = 1.f / sqrtf(s.x / gw + c.eps), m = s.y * rstd / gw;
 #pragma unroll
         for (int q = 0; q < VPT; ++q) {
             const int k = (q * TPR + t) * V;
             if (!in || k >= gw) continue;
-            float a[V], dy[V], dz[V];
-            if (c.scale) load_v<float, V, WIDE>(c.scale + g0 + k, a);
+            float dy[V], dz[V];
+            if (c.scale) {
+                float a[V];
+                cd[q].get(a);
+#pragma unroll
+                for (int v = 0; v < V; ++v) ds[q][v] = fmaf(a[v], y[q][v] * gate[q][v] * (rstd * w[q][v]), ds[q][v]);
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float sg = c.z ? sigmoid_f(z[q][v]) : 1.f, gate = c.z ? z[q][v] * sg : 1.f;
-                const float dgate = sg * fmaf(z[q][v], 1.f - sg, 1.f);  // silu'(z)
-                const float n = (c.norm_first ? y[q][v] : y[q][v] * gate) * rstd;
-                const float normed = n * w[q][v];
-                if (c.scale) ds[q][v] = fmaf(d[q][v], c.norm_first ? normed * gate : normed, ds[q][v]);
-                const float dg = c.scale ? d[q][v] * a[v] : d[q][v];  // at the norm's (gated) result
-                const float dm = c.norm_first ? dg * gate : dg;
-                dw[q][v] = fmaf(dm, n, dw[q][v]);
-                const float dv = rstd * (dm * w[q][v] - n * m);
-                dy[v] = c.norm_first ? dv : dv * gate;
-                dz[v] = (c.norm_first ? dg * normed : dv * y[q][v]) * dgate;
+                const float dgate = fmaf(gate[q][v], 1.f - sg[q][v], sg[q][v]);  // silu'(z)
+                if (FIRST) {
+                    const float n = y[q][v] * rstd, dm = d[q][v] * gate[q][v];
+                    dw[q][v] = fmaf(dm, n, dw[q][v]);
+                    dy[v] = rstd * fmaf(dm, w[q][v], -n * m);
+                    dz[v] = d[q][v] * n * (w[q][v] * dgate);
+                } else {
+                    const float n = y[q][v] * gate[q][v] * rstd;
+                    dw[q][v] = fmaf(d[q][v], n, dw[q][v]);
+                    const float dv = rstd * fmaf(d[q][v], w[q][v], -n * m);
+                    dy[v] = dv * gate[q][v];
+                    dz[v] = dv * y[q][v] * dgate;
+                }
             }
             const size_t o = (size_t)row * c.width + g0 + k;
             store_v<T, V, WIDE>(static_cast<T *>(c.dx) + o, dy);
@@ -320,25 +383,30 @@ __global__ void __launch_bounds__(block_threads<TPR>()) norm_after_bwd_kernel(No
     put_parts<V, VPT, TPR>(dw, ds, c.scale != nullptr, g0, gw, c.width, part, sums);
 }
 
-// dw (blockIdx.y 0) or dscale (1) from the blocks' parts.
-__global__ void __launch_bounds__(256) norm_bwd_sum(const float *__restrict__ part, int parts, int width,
-                                                   float *__restrict__ dw, float *__restrict__ ds) {
-    __shared__ float s[8][33];
-    const int k = blockIdx.x * 32 + (threadIdx.x & 31), q = threadIdx.x >> 5;
+// dw (blockIdx.y 0) or dscale (1) from the blocks' parts: 32 warps take every 32nd.
+__global__ void __launch_bounds__(1024) norm_bwd_sum(const float *__restrict__ part, int parts, int width,
+                                                    float *__restrict__ dw, float *__restrict__ ds) {
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5, k = blockIdx.x * 32 + lane;
     const float *p = part + (size_t)blockIdx.y * parts * width;
     float a = 0.f;
     if (k < width)
-        for (int i = q; i < parts; i += 8) a += p[(size_t)i * width + k];
-    s[q][threadIdx.x & 31] = a;
+#pragma unroll 8
+        for (int i = q; i < parts; i += 32) a += p[(size_t)i * width + k];
+    s[q][lane] = a;
     __syncthreads();
-    if (q || k >= width) return;
-    for (int i = 1; i < 8; ++i) a += s[i][threadIdx.x];
-    (blockIdx.y ? ds : dw)[k] = a;
+    a = s[lane][q];  // column q of the block
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (lane == 0 && blockIdx.x * 32 + q < width) (blockIdx.y ? ds : dw)[blockIdx.x * 32 + q] = a;
 }
 
 // Calls f with the unit's split: TPR threads (a power of two, MIN .. 512) of VPT
-// vectors of V channels.  One vector per thread up to 512 threads; four (then 16)
-// single channels where rows are not aligned vectors.
+// vectors of V channels; four (then 16) single channels where rows are not aligned
+// vectors.  Forwards a thread takes two vectors once there are enough units (up to 512
+// bf16 channels then stay in one warp: 8192 x 8 groups of 512 take 42.3 us, 49.6 us with
+// one vector; eight rows of 2048 4.6 us, 4.0 us with one).  Backwards it takes one where
+// 512 threads reach (with two the same groups took 118 us, 101 us with one).
 template <int VPT, int MIN, typename F> cudaError_t with_tpr(int vectors, F &&f) {
     const int need = (vectors + VPT - 1) / VPT;
     constexpr std::integral_constant<int, VPT> vpt{};
@@ -352,52 +420,55 @@ template <int VPT, int MIN, typename F> cudaError_t with_tpr(int vectors, F &&f)
         if (need <= 256) return f(vpt, std::integral_constant<int, 256>{});
     return f(vpt, std::integral_constant<int, 512>{});
 }
-template <int V, typename F> cudaError_t with_split(int width, F &&f) {
+template <int V, typename F> cudaError_t with_split(int width, bool two, F &&f) {
     static_assert(NORM_MAX_WIDTH == 8192, "the splits below end there");
     const int vectors = (width + V - 1) / V;
     if constexpr (V == 1) {
         return vectors <= 2048 ? with_tpr<4, 32>(vectors, f) : with_tpr<16, 256>(vectors, f);
     } else {
-        if (vectors <= 512) return with_tpr<1, 32>(vectors, f);
+        if (vectors <= (two ? 32 : 512)) return with_tpr<1, 32>(vectors, f);
         if constexpr (V == 4)
             if (vectors > 1024) return with_tpr<4, 512>(vectors, f);
-        return with_tpr<2, 512>(vectors, f);
+        return with_tpr<2, 32>(vectors, f);
     }
 }
 
 template <typename T, typename TR, int V> cudaError_t run_before(const NormCall &c, cudaStream_t st) {
-    return with_split<V>(c.width, [&](auto vpt, auto tpr) {
+    return with_split<V>(c.width, c.rows >= MANY_UNITS, [&](auto vpt, auto tpr) {
         constexpr int TH = block_threads<tpr()>(), U = TH / tpr();
         norm_before_kernel<T, TR, V, vpt(), tpr()><<<(c.rows + U - 1) / U, TH, 0, st>>>(c);
         return cudaGetLastError();
     });
 }
 template <typename T, int V> cudaError_t run_after(const NormCall &c, cudaStream_t st) {
-    return with_split<V>(c.width / c.groups, [&](auto vpt, auto tpr) {
+    return with_split<V>(c.width / c.groups, (long long)c.rows * c.groups >= MANY_UNITS, [&](auto vpt, auto tpr) {
         constexpr int TH = block_threads<tpr()>(), U = TH / tpr();
         norm_after_kernel<T, V, vpt(), tpr()><<<dim3((c.rows + U - 1) / U, c.groups), TH, 0, st>>>(c);
         return cudaGetLastError();
     });
 }
-int bwd_blocks(int rows, int units) { return min((rows + units - 1) / units, BWD_BLOCKS); }
+int bwd_blocks(int rows, int units, int threads, int groups) {
+    return min((rows + units - 1) / units, max(1, BWD_BLOCKS * 256 / threads / groups));
+}
 cudaError_t run_sum(const NormCall &c, const float *ws, int parts, cudaStream_t st) {
-    norm_bwd_sum<<<dim3((c.width + 31) / 32, c.scale ? 2 : 1), 256, 0, st>>>(ws, parts, c.width, c.dw, c.dscale);
+    norm_bwd_sum<<<dim3((c.width + 31) / 32, c.scale ? 2 : 1), 1024, 0, st>>>(ws, parts, c.width, c.dw, c.dscale);
     return cudaGetLastError();
 }
 template <typename T, typename TR, int V> cudaError_t run_before_bwd(const NormCall &c, float *ws, cudaStream_t st) {
-    return with_split<V>(c.width, [&](auto vpt, auto tpr) {
+    return with_split<V>(c.width, false, [&](auto vpt, auto tpr) {
         constexpr int TH = block_threads<tpr()>(), U = TH / tpr();
-        const int blocks = bwd_blocks(c.rows, U);
+        const int blocks = bwd_blocks(c.rows, U, TH, 1);
         if (blocks > 0) norm_before_bwd_kernel<T, TR, V, vpt(), tpr()><<<blocks, TH, 0, st>>>(c, ws);
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? run_sum(c, ws, blocks, st) : e;
     });
 }
 template <typename T, int V> cudaError_t run_after_bwd(const NormCall &c, float *ws, cudaStream_t st) {
-    return with_split<V>(c.width / c.groups, [&](auto vpt, auto tpr) {
+    return with_split<V>(c.width / c.groups, false, [&](auto vpt, auto tpr) {
         constexpr int TH = block_threads<tpr()>(), U = TH / tpr();
-        const int blocks = bwd_blocks(c.rows, U);
-        if (blocks > 0) norm_after_bwd_kernel<T, V, vpt(), tpr()><<<dim3(blocks, c.groups), TH, 0, st>>>(c, ws);
+        const int blocks = bwd_blocks(c.rows, U, TH, c.groups);
+        if (blocks > 0 && c.norm_first) norm_after_bwd_kernel<T, V, vpt(), tpr(), true><<<dim3(blocks, c.groups), TH, 0, st>>>(c, ws);
+        if (blocks > 0 && !c.norm_first) norm_after_bwd_kernel<T, V, vpt(), tpr(), false><<<dim3(blocks, c.groups), TH, 0, st>>>(c, ws);
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? run_sum(c, ws, blocks, st) : e;
     });
@@ -424,7 +495,9 @@ cudaError_t launch_norm_after(const NormCall &c, cudaStream_t st) {
     if (!c.bf16) return wide_rows(c, 4) ? run_after<float, 4>(c, st) : run_after<float, 1>(c, st);
     return wide_rows(c, 8) ? run_after<H, 8>(c, st) : run_after<H, 1>(c, st);
 }
-size_t norm_bwd_workspace(int rows, int width) { return 2 * (size_t)min(rows, BWD_BLOCKS) * width * sizeof(float); }
+size_t norm_bwd_workspace(int rows, int width) {  // blocks have 128 threads at least
+    return 2 * (size_t)min(rows, 2 * BWD_BLOCKS) * width * sizeof(float);
+}
 cudaError_t launch_norm_before_bwd(const NormCall &c, float *ws, cudaStream_t st) {
     using H = __nv_bfloat16;
     if (!c.bf16) return wide_rows(c, 4) ? run_before_bwd<float, float, 4>(c, ws, st) : run_before_bwd<float, float, 1>(c, ws, st);

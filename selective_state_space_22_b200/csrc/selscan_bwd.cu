@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
                         v[k] = e.x + e.y;
                     }
                     sums.add(v, 2 * (s - s2) + 1, lane);
-                    float2 G = sh.G[s][tid], dA = sh.dA[s][tid];
+                    float2 G = sh.G[s][tid], dA = make_float2(0.f, 0.f);  // of these tokens: one addition to the long sum
 #pragma unroll
                     for (int k = SUB - 1; k >= 0; --k) {
                         const float4 bc = q[k * NP];
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
                         const float2 e = mul2(u2[k], g);
                         v[k] = e.x + e.y;
                     }
-                    sh.G[s][tid] = G, sh.dA[s][tid] = dA;
+                    sh.G[s][tid] = G, sh.dA[s][tid] = add2(sh.dA[s][tid], dA);
                     sums.add(v, 2 * (s - s2), lane);
                 }
                 const int which = lane & 1, state = n0 + s2 + ((lane >> 1) & 1);  // what instruction lane%4 summed

@@ -52,6 +52,7 @@ def declare_mixer(lib):
 
 _same = contextlib.nullcontext()
 _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream  # without the lazy-init wrappers
+_empty = torch.empty
 _calls = {}
 
 
@@ -140,7 +141,7 @@ def _sequences(cu_seqlens, dev):
 
 
 def _scratch(nbytes, dev):
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    return _empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
 
 
 def _size(name, *sizes):
@@ -156,9 +157,17 @@ def _fresh(out, name, shape, dtype, dev):
     """out[name] checked, or a new tensor put there."""
     t = out.get(name)
     if t is None:
-        t = out[name] = torch.empty(shape, dtype=dtype, device=dev)
+        t = out[name] = _empty(shape, dtype=dtype, device=dev)
         return t.data_ptr()
     return _whole(t, name, dtype, dev, shape)
+
+
+def _given_or_new(t, name, like, shape):
+    """(tensor, data pointer) of an output: the given one checked, or a new one of like's dtype."""
+    if t is None:
+        t = like.new_empty(shape)
+        return t, t.data_ptr()
+    return t, _whole(t, name, like.dtype, like.device, shape)
 
 
 # ------------------------------------------------------------------ convolution
@@ -308,14 +317,13 @@ def ssd_selective_scan_varlen(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bia
         sp, slp, nslots = _states(state, slots, nseq, d, N, dev)
     hip = _maybe(has_init, "has_init", torch.bool, dev, (nseq,))
     with _on(dev, stream):
-        if y is None:
-            y = x.new_empty((n, d))
+        y, yp = _given_or_new(y, "y", x, (n, d))
         kept = None
         if return_chunk_states:
             kept = torch.empty((_size("ssd_selective_scan_chunk_states", n, nseq), N, d), dtype=_f32, device=dev)
         nbytes = _size("ssd_selective_scan_workspace_size", n, nseq, d, N)
         ws = _scratch(nbytes, dev)
-        check(f(a, cu, sp, slp, hip, None if kept is None else kept.data_ptr(), _whole(y, "y", x.dtype, dev, (n, d)), n,
+        check(f(a, cu, sp, slp, hip, None if kept is None else kept.data_ptr(), yp, n,
                 nseq, nslots, None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev.index)))
     return y, kept
 
@@ -331,9 +339,8 @@ def ssd_selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=No
     _device_of(state, "state")
     sp, slp, nslots = _states(state, slots, n, d, N, dev)
     with _on(dev, stream):
-        if y is None:
-            y = x.new_empty((n, d))
-        check(f(a, sp, slp, _whole(y, "y", x.dtype, dev, (n, d)), n, nslots, _raw_stream(dev.index)))
+        y, yp = _given_or_new(y, "y", x, (n, d))
+        check(f(a, sp, slp, yp, n, nslots, _raw_stream(dev.index)))
     return y
 
 
@@ -381,12 +388,9 @@ def ssd_residual_rmsnorm(x, weight, residual=None, scale=None, *, eps=1e-5, out=
     xp, ldx = _rows(x, "x", t, dev, shape)
     wp, sp = _whole(weight, "weight", _f32, dev, (d,)), _maybe(scale, "scale", _f32, dev, (d,))
     with _on(dev, stream):
-        if out is None:
-            out = x.new_empty(shape)
-        if residual_out is None:
-            residual_out = x.new_empty(shape, dtype=rt)
-        check(f(xp, ldx, rp, ldr, sp, wp, _whole(out, "out", t, dev, shape), _whole(residual_out, "residual_out", rt, dev, shape),
-                io, _IO[rt], n, d, eps, _raw_stream(dev.index)))
+        out, op = _given_or_new(out, "out", x, shape)
+        residual_out, rop = _given_or_new(residual_out, "residual_out", x if residual is None else residual, shape)
+        check(f(xp, ldx, rp, ldr, sp, wp, op, rop, io, _IO[rt], n, d, eps, _raw_stream(dev.index)))
     return out, residual_out
 
 
@@ -444,10 +448,9 @@ def ssd_gated_rmsnorm(y, z, weight, residual=None, scale=None, *, ngroups=1, nor
     dev, io, shape, yp, ldy, zp, ldz, wp, sp = _gated_inputs(y, z, weight, scale)
     rp, ldr = (None, 0) if residual is None else _rows(residual, "residual", y.dtype, dev, shape)
     with _on(dev, stream):
-        if out is None:
-            out = y.new_empty(shape)
-        check(f(yp, ldy, zp, ldz, rp, ldr, sp, wp, _whole(out, "out", y.dtype, dev, shape), io, *shape, ngroups,
-                bool(norm_before_gate), eps, _raw_stream(dev.index)))
+        out, op = _given_or_new(out, "out", y, shape)
+        check(f(yp, ldy, zp, ldz, rp, ldr, sp, wp, op, io, *shape, ngroups, bool(norm_before_gate), eps,
+                _raw_stream(dev.index)))
     return out
 
 
