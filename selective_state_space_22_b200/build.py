@@ -1,4 +1,5 @@
-"""Build libssd.so (CUDA for sm_100a) in-tree with nvcc.
+"""Build libssd.so (CUDA for sm_100a, with nvcc) and the native Python binding
+_bind.so (with g++, against torch's headers) in-tree.
 
 Each ``csrc/*.cu`` file is compiled separately (in parallel) into ``_build/``
 and linked into ``selective_state_space_22_b200/libssd.so``.  The CUDA runtime
@@ -23,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libssd.so")
+BIND = os.path.join(PKG, "_bind.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
@@ -51,8 +53,23 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _bind_command() -> list[str]:
+    import sysconfig
+
+    import torch
+
+    t = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [INCLUDE, os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    lib = os.path.join(t, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f"-I{i}" for i in inc], os.path.join(CSRC, "bind.cpp"), "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python", f"-Wl,-rpath,{lib}"]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every kernel source for sm_100a and link libssd.so; return its path."""
+    """Compile every kernel source for sm_100a, link libssd.so and the binding; return the library's path."""
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
@@ -67,17 +84,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if verbose:
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)
+    bind_tmp = None
+    if force or _stale(BIND, [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "ssd.h"), __file__]):
+        bind_tmp = BIND + f".tmp{os.getpid()}"
+        jobs.append([*_bind_command(), "-o", bind_tmp])
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
         return r.stdout + r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, max(1, len(jobs)))) as ex:
         for out in ex.map(run, jobs):
             if verbose and out:
                 print(out)
+    if bind_tmp:
+        os.replace(bind_tmp, BIND)
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
