@@ -20,7 +20,7 @@ namespace ssd {
 namespace {
 
 constexpr int AHEAD = 8;  // tokens at a time, and fetched ahead
-constexpr int FWD_BLOCKS_PER_SM = 8;
+constexpr int FWD_BLOCKS_PER_SM = 4;
 
 template <int NP> struct FwdLanes {
     static constexpr int NS = NP < 8 ? NP : 8, P = NS / 2, SPLIT = NP / NS, CHANS = 32 / SPLIT, OWN = AHEAD / SPLIT;

@@ -27,7 +27,7 @@
 namespace ssd {
 namespace {
 
-constexpr int SUB = GROUP, BWD_BLOCKS_PER_SM = 8;
+constexpr int SUB = GROUP, BWD_BLOCKS_PER_SM = 4;
 static_assert(SEL_CHUNK == 2 * SUB, "a chunk is two halves");
 
 // Sums over a warp's channels by matrix instructions: D[lane/4][c] += A[lane/4][k] B[k][c],

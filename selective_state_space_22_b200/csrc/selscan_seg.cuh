@@ -69,7 +69,7 @@ constexpr int GROUP = 4;
 template <int NP> struct Lanes {
     static constexpr int NS = NP < 8 ? NP : NP <= 32 ? 8 : 16, SPLIT = NP / NS, PAIRS = 32 / SPLIT, CH = 64 / SPLIT;  // CH: channels of a warp
 };
-constexpr int SCAN_THREADS = 64;
+constexpr int SCAN_THREADS = 128;  // of a block: 64 measured 10 % more at 64 x 512 tokens (B and C staged for fewer channels), 256 7 %
 
 __device__ __forceinline__ void cp16(void *smem, const void *gmem) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem)

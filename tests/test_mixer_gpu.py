@@ -382,3 +382,211 @@ def test_conv_sees_no_row_past_its_width(K, cx):
         touched[:] = False
         touched[max(t0 - K + 1, lo):t0 + 1] = True
         assert torch.equal(~torch.isfinite(dx).all(1), touched)
+
+
+# ---------------------------------------------------- together, as they are used
+
+def test_prompt_then_tokens_is_the_whole_sequence():
+    """A Mamba-1 mixer as serving runs it: prompts into slots (conv, scan), then a token
+    at a time, against one run over the whole sequences."""
+    g, d, N, K = gen(31), 48, 16, 4
+    lens, more, nslots = [37, 1, 200], 5, 6
+    whole = [n + more for n in lens]
+    n = sum(whole)
+    xz = randn(g, n, 2 * d, io=torch.bfloat16)
+    proj = randn(g, n, 8 + 2 * N, io=torch.bfloat16)  # the x projection's output: dt rank, B, C
+    dt = randn(g, n, d, io=torch.bfloat16, scale=0.7)
+    w, b, A = randn(g, d, K, scale=0.5), randn(g, d, scale=0.1), -(torch.rand(d, N, generator=g) * 15 + 1).cuda()
+    D, bias, norm = randn(g, d), randn(g, d, scale=0.5) - 2.5, 1 + randn(g, d, scale=0.1)
+    B, C = proj[:, 8:8 + N].unflatten(1, (1, N)), proj[:, 8 + N:].unflatten(1, (1, N))
+
+    def mixer(rows, cu=None, states=None, slots=None):
+        conv_state, state = states
+        args = dict(slots=slots)
+        xin, z = xz[rows, :d], xz[rows, d:]
+        if cu is None:
+            x = ssd.ssd_conv1d_update(conv_state, xin, w, b, **args)[0]
+            y = ssd.ssd_selective_state_update(state, x, dt[rows], A, B[rows], C[rows], D, z, bias, **args)
+        else:
+            x = ssd.ssd_conv1d_varlen(xin, w, b, cu, conv_state=conv_state, **args)[0]
+            y, _ = ssd.ssd_selective_scan_varlen(x, dt[rows], A, B[rows], C[rows], cu, D, z, bias, state=state, **args)
+        return ssd.ssd_gated_rmsnorm(y, None, norm)
+
+    fresh = lambda: (torch.full((nslots, d, K - 1), float("nan"), dtype=torch.bfloat16, device="cuda"),  # noqa: E731
+                     torch.full((nslots, d, N), float("nan"), device="cuda"))
+    all_rows = slice(0, n)
+    whole_states = fresh()
+    want = mixer(all_rows, bounds(whole), whole_states, torch.arange(3, dtype=torch.int32, device="cuda"))
+    first = torch.tensor([0] + whole).cumsum(0)
+    prompt = torch.cat([torch.arange(first[i], first[i] + lens[i]) for i in range(3)]).cuda()
+    states, slots = fresh(), torch.tensor([4, 0, 3], dtype=torch.int32, device="cuda")
+    got = torch.empty_like(want)
+    got[prompt] = mixer(prompt, bounds(lens), states, slots)
+    for step in range(more):
+        rows = torch.tensor([int(first[i]) + lens[i] + step for i in range(3)], device="cuda")
+        got[rows] = mixer(rows, None, states, slots)
+    ssd.ssd_get_device_status()
+    # the same float32 recurrence cut at other places; then two bf16 roundings (y and the norm)
+    # and what the first one does to the second
+    scale = want.float().abs().amax()
+    assert (got.float() - want.float()).abs().max() <= 4 * 2.0 ** -8 * scale
+    assert (got == want).float().mean() > 0.9
+    for a, b in zip(states, whole_states):
+        assert torch.allclose(a[slots.long()].float(), b[:3].float(), rtol=1e-5, atol=1e-5)
+
+
+def test_training_chain_against_differences():
+    """norm before -> conv -> scan -> norm after, packed, float32: the gradients chained by
+    hand against central differences of the chained forwards."""
+    g, d, N, lens = gen(41), 24, 8, [50, 1, 30]
+    n, cu = sum(lens), bounds(lens)
+    p = dict(r=randn(g, n, d), w0=1 + randn(g, d, scale=0.1), w=randn(g, d, 4, scale=0.5), b=randn(g, d, scale=0.1),
+             dt=randn(g, n, d, scale=0.7), A=-(torch.rand(d, N, generator=g) * 7 + 1).cuda(), B=randn(g, n, 1, N), C=randn(g, n, 1, N),
+             D=randn(g, d), z=randn(g, n, d), bias=randn(g, d, scale=0.5) - 2, w1=1 + randn(g, d, scale=0.1))
+    up = randn(g, n, d)
+
+    def forward(r, w0, w, b, dt, A, B, C, D, z, bias, w1):
+        h, res = ssd.ssd_residual_rmsnorm(r, w0)
+        x = ssd.ssd_conv1d_varlen(h, w, b, cu)[0]
+        y, kept = ssd.ssd_selective_scan_varlen(x, dt, A, B, C, cu, D, z, bias, return_chunk_states=True)
+        return ssd.ssd_gated_rmsnorm(y, z, w1), (h, res, x, y, kept)
+
+    _, (h, res, x, y, kept) = forward(**p)
+    ga = ssd.ssd_gated_rmsnorm_bwd(y, p["z"], p["w1"], up)
+    gs = ssd.ssd_selective_scan_bwd(x, p["dt"], p["A"], p["B"], p["C"], cu, ga["dy"], kept, p["D"], p["z"], p["bias"])
+    gc = ssd.ssd_conv1d_bwd(h, p["w"], p["b"], cu, gs["dx"])
+    gb = ssd.ssd_residual_rmsnorm_bwd(res, p["w0"], gc["dxbc"])
+    grads = dict(r=gb["dx"], w0=gb["dweight"], w=gc["dweight"], b=gc["dbias"], dt=gs["ddt"], A=gs["dA"], B=gs["dB"], C=gs["dC"],
+                 D=gs["dD"], z=gs["dz"] + ga["dz"], bias=gs["ddt_bias"], w1=ga["dweight"])
+    loss = lambda q: (forward(**q)[0].double() * up.double()).sum().item()  # noqa: E731
+    eps = 2.0 ** -7  # the difference's own error: eps^2 of a third derivative, and 2^-24 sum |out up| / eps
+    noise = (forward(**p)[0].double() * up.double()).abs().sum().item() * 2.0 ** -20 / eps
+    for k, v in p.items():
+        v_dir = torch.randn(v.shape, generator=g).cuda() * (0.1 if k in ("A", "dt", "bias") else 1.0) / v.numel() ** 0.5
+        slope = (grads[k].double() * v_dir.double()).sum().item()
+        diff = (loss(dict(p, **{k: v + eps * v_dir})) - loss(dict(p, **{k: v - eps * v_dir}))) / (2 * eps)
+        assert abs(diff - slope) <= 1e-2 * abs(slope) + noise + 1e-3, (k, diff, slope)
+
+
+def test_bad_bounds_and_slots_are_reported_and_harmless():
+    """Bounds that leave the tensor, slots out of range or named twice: nothing outside is
+    touched, the rest is served, and the status says so once."""
+    g, d, N, n = gen(51), 40, 16, 60
+    ins, opt = sel_inputs(g, n, d, 1, N, torch.float32, 0)
+    w = randn(g, d, 4)
+
+    def reported():
+        with pytest.raises(ssd.SSDError) as e:
+            ssd.ssd_get_device_status()
+        assert e.value.status == ssd.SSD_ERR_INVALID_ARG
+        ssd.ssd_get_device_status()  # cleared
+
+    good = ssd.ssd_selective_scan_varlen(*ins, bounds([20]), *opt)[0][:20]
+    for cu in ([0, 20, 70], [-5, 20, 40], [0, 20, 10], [20, 0, 20], [0, 20, 2 ** 31 - 1], [0, 20, -2 ** 31]):
+        cu = torch.tensor(cu, dtype=torch.int32).cuda()
+        y = torch.full((n, d), 7.0, device="cuda")
+        _, kept = ssd.ssd_selective_scan_varlen(*ins, cu, *opt, y=y, return_chunk_states=True)
+        if cu[0] == 0 and cu[1] == 20:
+            assert torch.equal(y[:20], good)
+        reported()
+        ssd.ssd_selective_scan_bwd(*ins, cu, torch.ones_like(y), kept, *opt)
+        reported()
+        for call in (lambda: ssd.ssd_conv1d_varlen(ins[0], w, None, cu), lambda: ssd.ssd_conv1d_bwd(ins[0], w, None, cu, ins[0])):
+            call()
+            reported()
+    state, conv_state = torch.zeros(3, d, N, device="cuda"), torch.zeros(3, d, 3, device="cuda")
+    cu, lens3 = bounds([20, 20, 20]), 3
+    for slots in ([1, 3, 0], [1, 1, 0], [2, 0, 2 ** 31 - 1]):
+        s = torch.tensor(slots, dtype=torch.int32).cuda()
+        served = [v for v in dict.fromkeys(slots) if v < 3]
+        for t in (state, conv_state):
+            t.fill_(0.25)
+        ssd.ssd_selective_scan_varlen(*ins, cu, *opt, state=state, slots=s)
+        reported()
+        ssd.ssd_conv1d_varlen(ins[0], w, None, cu, conv_state=conv_state, slots=s)
+        reported()
+        for t in (state, conv_state):
+            for v in range(3):
+                assert (t[v] == 0.25).all().item() == (v not in served), (slots, v)
+        t3 = [t[:lens3] for t in ins[:2]] + [ins[2]] + [t[:lens3] for t in ins[3:]]
+        o3 = (opt[0], opt[1][:lens3], opt[2])
+        for t in (state, conv_state):
+            t.fill_(0.25)
+        y = torch.full((lens3, d), 7.0, device="cuda")
+        ssd.ssd_selective_state_update(state, *t3, *o3, slots=s, y=y)
+        reported()
+        x = torch.full((lens3, d), 7.0, device="cuda")
+        ssd.ssd_conv1d_update(conv_state, ins[0][:lens3], w, slots=s, out=(x, x[:, :0].contiguous(), x[:, :0].contiguous()))
+        reported()
+        for t in (state, conv_state):
+            for v in range(3):
+                assert (t[v] == 0.25).all().item() == (v not in served), (slots, v)
+        skipped = [i for i in range(3) if slots[i] >= 3 or slots[i] in slots[:i]]
+        for i in range(3):
+            assert (y[i] == 7).all().item() == (i in skipped) and (x[i] == 7).all().item() == (i in skipped)
+
+
+def test_on_streams_and_in_graphs():
+    """Two streams at once and two captured graphs (each with its own scratch) give the
+    bits of plain calls; a graph sees the inputs of its replay."""
+    g, d, N, lens = gen(61), 96, 16, [3000, 200]  # few channels, long: cut into segments, with scratch
+    n, cu = sum(lens), bounds(lens)
+    sets = [sel_inputs(g, n, d, 1, N, torch.bfloat16, 0) for _ in range(2)]
+    dy = randn(g, n, d, io=torch.bfloat16)
+
+    def step(ins, opt, **kw):
+        y, kept = ssd.ssd_selective_scan_varlen(*ins, cu, *opt, return_chunk_states=True, **kw)
+        return [y] + list(ssd.ssd_selective_scan_bwd(*ins, cu, dy, kept, *opt, **kw).values())
+
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = [step(*s, stream=st) for s, st in zip(sets, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for w, v in zip(want, got) for a, b in zip(w, v))
+    graphs, outs = [], []
+    for s in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(step(*s))
+        graphs.append(graph)
+    for order in ((0, 1), (1, 0)):
+        for k in order:
+            graphs[k].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for w, v in zip(want, outs) for a, b in zip(w, v))
+    sets[0][0][0].copy_(sets[1][0][0])  # another x
+    again = step(*sets[0])
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(again, outs[0]))
+    ssd.ssd_get_device_status()
+
+
+def test_given_outputs_are_used_and_checked():
+    g, n, d = gen(71), 9, 32
+    x, w = randn(g, n, d), 1 + randn(g, d, scale=0.1)
+    out, res = torch.empty_like(x), torch.empty_like(x)
+    a, b = ssd.ssd_residual_rmsnorm(x, w, x, out=out, residual_out=res)
+    assert a is out and b is res
+    grads = dict(dresidual=torch.empty_like(x), dweight=torch.empty_like(w))
+    got = ssd.ssd_residual_rmsnorm_bwd(res, w, x, out=grads)
+    assert got is grads and got["dx"] is grads["dresidual"]
+    for bad in (lambda: ssd.ssd_residual_rmsnorm(x, w, out=out[:, :16]), lambda: ssd.ssd_residual_rmsnorm(x, w.half()),
+                lambda: ssd.ssd_residual_rmsnorm(x.half(), w), lambda: ssd.ssd_residual_rmsnorm(x.T, w), lambda: ssd.ssd_residual_rmsnorm(x, w, x.cpu()),
+                lambda: ssd.ssd_residual_rmsnorm(x, None), lambda: ssd.ssd_residual_rmsnorm(x[0], w), lambda: ssd.ssd_gated_rmsnorm(x, x, w[:5]),
+                lambda: ssd.ssd_residual_rmsnorm_bwd(x, w, x, scale=w), lambda: ssd.ssd_conv1d_varlen(x, w[:, None], None, bounds([n]).long()),
+                lambda: ssd.ssd_conv1d_varlen(x, w[:, None], None, bounds([n]), x_channels=5), lambda: ssd.ssd_conv1d_varlen(x[:, ::2], w[::2, None], None, bounds([n])),
+                lambda: ssd.ssd_conv1d_varlen(x.expand(n, d), w[:, None], None, bounds([n]), out=(out,))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: ssd.ssd_gated_rmsnorm(x, x, w, ngroups=3), lambda: ssd.ssd_gated_rmsnorm(x, x, w, eps=-1.0),
+                lambda: ssd.ssd_residual_rmsnorm(x, torch.ones(d + 1, device="cuda")[1:])):
+        with pytest.raises(ssd.SSDError):
+            bad()
+    empty = x[:0]
+    assert ssd.ssd_residual_rmsnorm(empty, w)[0].shape == (0, d) and ssd.ssd_gated_rmsnorm(empty, empty, w).shape == (0, d)
+    assert ssd.ssd_conv1d_varlen(empty, w[:, None].contiguous(), None, bounds([]))[0].shape == (0, d)
+    none = ssd.ssd_conv1d_bwd(empty, w[:, None].contiguous(), None, bounds([]), empty)
+    assert (none["dweight"] == 0).all()
