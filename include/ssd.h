@@ -473,7 +473,7 @@ typedef struct {
  * cut is carried over exactly like the states of ssd_fold_states).
  *  state  [nslots, channels, dstate] float32, or NULL: every sequence from zero
  *  chunk_states  NULL, or [ssd_selective_scan_chunk_states(tokens, nseq), dstate,
- *         channels] float32: the states before every 16th token of each sequence,
+ *         channels] float32: the states before every 8th token of each sequence,
  *         which ssd_selective_scan_bwd reads (entries of no sequence stay unwritten)
  *  y      [tokens, channels] io_dtype, contiguous
  */

@@ -1,7 +1,7 @@
 // bind.cpp -- the Python binding of the mixer-block operators (mixer.py): checks of the
 // tensors, outputs and scratch, and the call of the C entry point, in one native step.
-// A call costs about 5 us of host time beside the launch this way, 10 from Python; for
-// one token or a few rows that is most of what a call takes.
+// A call on one token of a 1024-channel scan takes 4.8 us this way, launch included, 14.8 us
+// from Python.
 //
 // The C entry points' addresses come from the library that the package has loaded
 // (bind()), so this module neither links nor finds libssd itself.  A function returns
@@ -453,8 +453,10 @@ PyObject *residual_rmsnorm_bwd(PyObject *const *a) {
     const auto *w = static_cast<const float *>(c.whole(a[1], "weight", at::kFloat, {d})), *sc = static_cast<const float *>(c.maybe(a[5], "scale", at::kFloat, {d}));
     const void *up = c.whole(dout, "dout", type, shape), *ur = c.maybe(a[3], "dresidual", rtype, shape);
     Outputs out(a[7]);
-    const Tensor gr = out.tensor_of(c, "dresidual", rtype, shape), gx = apart ? out.tensor_of(c, "dx", type, shape) : Tensor();
-    if (!apart) out.set("dx", wrap(gr));
+    const Tensor gr = out.tensor_of(c, "dresidual", rtype, shape);
+    PyObject *given = PyDict_GetItemString(out.d, "dx");  // a tensor of the caller's is filled in any case
+    const Tensor gx = apart || !none(given) ? out.tensor_of(c, "dx", type, shape) : Tensor();
+    if (!gx.defined()) out.set("dx", wrap(gr));
     const Tensor gw = out.tensor_of(c, "dweight", at::kFloat, {d}), gs = scaled ? out.tensor_of(c, "dscale", at::kFloat, {d}) : Tensor();
     if (!scaled) out.absent("dscale");
     const size_t bytes = sized(entry.ssd_rmsnorm_bwd_workspace_size(n, d), "the norm's gradient");

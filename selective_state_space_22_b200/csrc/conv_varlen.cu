@@ -66,8 +66,9 @@ __device__ __forceinline__ Dst<T, V> out_of(T *xo, T *bo, T *co, int c, int cx, 
 }
 
 // A run's next BATCH rows, fetched ahead as they lie in memory.  (All 35 rows copied
-// into shared memory at once instead measured 44.5 us against 39.8 us for 9408 x 4352
-// bf16: the rows were not late, and 16 KB more per block cost occupancy.)
+// into shared memory at once instead measured 44.5 us for 9408 x 4352 bf16 where this
+// form took 39.8 us, 34 us since: the rows were not late, and 16 KB more per block cost
+// occupancy.)
 template <typename T, int V> struct Ahead {
     static constexpr int BATCH = sizeof(T) * V == 16 ? 4 : 8;
     using Vec = typename std::conditional<V == 1, T, typename std::conditional<sizeof(T) * V == 16, uint4, uint2>::type>::type;

@@ -111,6 +111,21 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 
+// 2^x for |x| <= SMALL_EXP by its Taylor polynomial (the first term left out is below
+// 8e-9): decays near one come out to within an ulp, where the approximate exponential is
+// off by up to about 2^-22, mostly to the same side.
+constexpr float SMALL_EXP = 1.f;
+__device__ __forceinline__ float2 ex2_small(float2 x) {
+    float2 p = fma2(x, splat(1.0178086009e-7f), splat(1.3215486790e-6f));  // ln2^9 / 9!, ln2^8 / 8!
+    p = fma2(x, p, splat(1.5252733804e-5f));
+    p = fma2(x, p, splat(1.5403530393e-4f));
+    p = fma2(x, p, splat(1.3333558146e-3f));
+    p = fma2(x, p, splat(9.6181291076e-3f));
+    p = fma2(x, p, splat(5.5504108665e-2f));
+    p = fma2(x, p, splat(2.4022650696e-1f));
+    p = fma2(x, p, splat(6.9314718056e-1f));
+    return fma2(x, p, splat(1.f));
+}
 __device__ __forceinline__ float2 silu2(float2 v) {
     const float2 e = mul2(v, splat(-LOG2E)), d = add2(make_float2(ex2a(e.x), ex2a(e.y)), splat(1.f));
     return mul2(v, make_float2(rcpa(d.x), rcpa(d.y)));

@@ -75,8 +75,8 @@ ssd_status check_sel(ssd_dtype io, int channels, int ngroups, int dstate) {
     if (channels % ngroups) return refuse(SSD_ERR_INVALID_ARG, "ngroups (%d) must divide channels (%d)", ngroups, channels);
     if (dstate > ssd::SEL_MAX_DSTATE)
         return refuse(SSD_ERR_UNSUPPORTED, "dstate must be at most %d (got %d)", ssd::SEL_MAX_DSTATE, dstate);
-    // grid: at least 8 channels of one group per block
-    if (ngroups * ((channels / ngroups + 7LL) / 8) > 65535) return refuse(SSD_ERR_UNSUPPORTED, "too many channels for the grid");
+    // grid.y: a block takes at least 16 channels of one group (dstate 64, four lanes or more a channel)
+    if (ngroups * ((channels / ngroups + 15LL) / 16) > 65535) return refuse(SSD_ERR_UNSUPPORTED, "too many channels for the grid");
     return SSD_OK;
 }
 

@@ -10,10 +10,11 @@
 // registers (neighbouring lanes, neighbouring channels), eight tokens ahead; B and C,
 // which a block's channels share, through shared memory.  Bound by the exponential
 // unit (N + 4 operations per channel and token at 16 per SM and clock), then by issue.
-// Measured at 64 x 512 tokens, 1024 channels, 16 states: KERNEL_TIME.  A form that split the
-// tokens of a chunk over the lanes of a warp (one exponential per state and token at any
-// length, but scans over lanes and a second walk) took 352 us, all states in one thread 318 us,
-// two channels to a packed operation 290 us.
+// Measured at 64 x 512 tokens, 1024 channels, 16 states, bf16, states kept: 258 us, 2.1 TB/s
+// and 58 % of the exponential unit.  A form that split the tokens of a chunk over the lanes
+// of a warp (one exponential per state and token at any length, but scans over lanes and a
+// second walk) took 352 us, all states in one thread 318 us, two channels to a packed
+// operation 290 us.
 #include "selscan_seg.cuh"
 
 namespace ssd {
@@ -222,9 +223,10 @@ __global__ void __launch_bounds__(128) sel_join_kernel(SelCall c, Segments sg, b
 // group go through their LP channels together, four states a lane (dstate = 4 LP), so
 // that a group reads and writes whole rows of the state, all loads first, and a lane
 // ends with its own channel's readout.  (LP lanes doing the scalar work of each of
-// their channels together measured 43.6 us against KERNEL us for 256 x 4096 channels
+// their channels together measured 43.6 us against 27.5 us for 256 x 4096 channels
 // of 16 states: five times the instructions.)  LP = 0: any dstate, a lane per channel.
-// SAME: the warp's channels lie in one B/C group.  Bound by HBM: the state in and out.
+// SAME: the warp's channels lie in one B/C group.  Bound by HBM: the state in and out
+// (27.5 us is 5.2 TB/s of the bytes that have to move).
 constexpr int UPD_THREADS = 128;
 template <typename T, int LP, bool SAME>
 __global__ void __launch_bounds__(UPD_THREADS) sel_update_kernel(SelCall c, bool wide_bc) {

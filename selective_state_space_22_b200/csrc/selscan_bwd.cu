@@ -8,8 +8,7 @@
 //   dz_t = dy_t p_t silu'(z_t),  ddt_t = ddelta_t softplus'(dt_t + bias),  dbias = sum_t ddt_t.
 //
 // A thread takes two channels and 8 states and walks its sequence (or segment,
-// selscan_seg.cuh) backwards, in
-// chunks of SEL_CHUNK tokens that start where the forward kept the states, and a chunk
+// selscan_seg.cuh) backwards, in chunks of SEL_CHUNK tokens that start where the forward kept the states, and a chunk
 // in two halves of SUB tokens.  For each half and state it runs the
 // recurrence forwards (a_t and h_{t-1} stay in registers, so the backward walk takes no
 // exponential) and then backwards, both channels in one packed operation; the second half
@@ -18,8 +17,8 @@
 // dB and dC are summed over a warp's channels by matrix instructions (ChannelSum), over
 // the block's warps in shared memory, and over blocks by sel_bwd_sum, all in a fixed
 // order.  Bound by issue and latency: the registers of a half (step, input and upstream
-// gradient of 8 tokens, three sums for each, a_t and h_{t-1}) leave 12 warps to an SM.
-// Measured at 64 x 512 tokens, 1024 channels, 16 states: KERNEL_TIME.  A form that split a
+// gradient of 4 tokens, three sums for each, a_t and h_{t-1}) leave 16 warps to an SM.
+// Measured at 64 x 512 tokens, 1024 channels, 16 states, bf16: 990 us.  A form that split a
 // chunk's tokens over the lanes of a warp took 1428 us, one with a channel per thread and
 // its states paired 1490 us (each step, input and gradient held twice, spilled).
 #include "selscan_seg.cuh"
@@ -107,7 +106,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Sh &sh = *reinterpret_cast<Sh *>(smem_raw);
     const Mine me = my_channels<NP>(c, blockIdx.y);
-    const int N = c.dstate, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = lane / PAIRS, pair = lane % PAIRS, n0 = part * NS;
+    const int N = c.dstate, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = lane / PAIRS, pair = lane % PAIRS;
+    auto state_of = [&](int k) { return k * SPLIT + part; };  // neighbours at the same time: A = -1, -2, .. are alike then
     const int ch = 2 * (warp * PAIRS + pair);  // of the block's
     const size_t step = (size_t)N * c.channels;
     float *const pa = parts.a + blockIdx.x * step, *const pdd = parts.d + (size_t)blockIdx.x * 2 * c.channels;
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
     int i, first, lo, hi, end;
     if (!segment(c.seq, sg.seg, blockIdx.x, i, first, lo, hi, end)) {  // the same for the whole block
         for (int k = 0; k < NS; ++k)
-            if (n0 + k < N) store_two<float>(pa + (size_t)(n0 + k) * c.channels, zero, me, ok.state);
+            if (state_of(k) < N) store_two<float>(pa + (size_t)state_of(k) * c.channels, zero, me, ok.state);
         if (part == 0) store_two<float>(pdd, zero, me, ok.state), store_two<float>(pdd + c.channels, zero, me, ok.state);
         return;
     }
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
     const float2 bias = c.dt_bias ? make_float2(c.dt_bias[me.c0], c.dt_bias[me.c1]) : zero;
     const float2 D = c.D ? make_float2(c.D[me.c0], c.D[me.c1]) : zero;
     for (int k = 0; k < NS; ++k) {
-        const int n = n0 + k;
+        const int n = state_of(k);
         float2 A2 = zero, G = zero;
         if (n < N) {
             A2 = make_float2(c.A[(size_t)me.c0 * N + n] * LOG2E, c.A[(size_t)me.c1 * N + n] * LOG2E);
@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
         fetch_rows<T, CH>(sh.dy, static_cast<const T *>(c.dy) + (size_t)t0 * c.channels + t_first, c.channels, n, t_cols, ok.wide);
 #pragma unroll
         for (int k = 0; k < NS; ++k) {
-            if (n0 + k >= N) continue;
-            const float *from = kept + chunk * step + (size_t)(n0 + k) * c.channels;
+            if (state_of(k) >= N) continue;
+            const float *from = kept + chunk * step + (size_t)state_of(k) * c.channels;
             if (ok.state) {
                 cp8(&sh.h0[k][tid], from + me.c0);
             } else {
@@ -184,6 +184,24 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
             for (int k = 0; k < SUB; ++k) w[k] = SPLIT == 1 ? v[k / SPLIT] : shfl2(v[k / SPLIT], pair + k % SPLIT * PAIRS);
         };
         float2 dl[SUB], u2[SUB], own_dl[OWN], own[OWN];
+        float most;  // the lane's largest step
+        // a[k] = exp(delta_k A). Decays near one, where the whole warp has them, by the
+        // polynomial: the gradient of the state adds up many of their errors (dA 1.2e-6 off
+        // with the approximate exponential everywhere, 6.3e-7 so, at 32 sequences of 512
+        // tokens; 64 of them take 907 and 990 us). The state before a second half is four
+        // tokens away from one that was kept, and does without.
+        auto decays = [&](float2 A2, float2 (&a)[SUB]) {
+            if (__all_sync(0xffffffffu, most * fmaxf(fabsf(A2.x), fabsf(A2.y)) <= SMALL_EXP)) {
+#pragma unroll
+                for (int k = 0; k < SUB; ++k) a[k] = ex2_small(mul2(dl[k], A2));
+            } else {
+#pragma unroll
+                for (int k = 0; k < SUB; ++k) {
+                    const float2 x = mul2(dl[k], A2);
+                    a[k] = make_float2(ex2a(x.x), ex2a(x.y));
+                }
+            }
+        };
         auto steps_of_half = [&](int k0) {
 #pragma unroll
             for (int j = 0; j < OWN; ++j) {
@@ -193,6 +211,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
             }
             spread(own_dl, dl);
             spread(own, u2);
+            most = 0.f;
+#pragma unroll
+            for (int k = 0; k < SUB; ++k) most = fmaxf(most, fmaxf(fabsf(dl[k].x), fabsf(dl[k].y)));
         };
         if (n > SUB) {  // the state before the second half
             steps_of_half(0);
@@ -202,7 +223,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
                 float2 h = sh.h0[s][tid];
 #pragma unroll
                 for (int k = 0; k < SUB; ++k) {
-                    const float2 b = *reinterpret_cast<const float2 *>(sh.bc + k * NP + n0 + s), arg = mul2(dl[k], A2);
+                    const float2 b = *reinterpret_cast<const float2 *>(sh.bc + k * NP + state_of(s)), arg = mul2(dl[k], A2);
                     h = fma2(make_float2(ex2a(arg.x), ex2a(arg.y)), h, mul2(u2[k], b));
                 }
                 sh.hm[s][tid] = h;
@@ -231,12 +252,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
                     const float2 A2 = sh.A2[s][tid];
                     float2 h = h_from[s][tid], a[SUB], hp[SUB];
                     float v[SUB];
-                    const float4 *q = sh.bc + k0 * NP + n0 + s;
+                    const float4 *q = sh.bc + k0 * NP + state_of(s);
+                    decays(A2, a);
 #pragma unroll
                     for (int k = 0; k < SUB; ++k) {
                         const float4 bc = q[k * NP];
-                        const float2 arg = mul2(dl[k], A2);
-                        a[k] = make_float2(ex2a(arg.x), ex2a(arg.y));
                         hp[k] = h;
                         h = fma2(a[k], h, mul2(u2[k], make_float2(bc.x, bc.y)));
                         pre[k] = fma2(make_float2(bc.z, bc.w), h, pre[k]);
@@ -260,7 +280,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
                     sh.G[s][tid] = G, sh.dA[s][tid] = add2(sh.dA[s][tid], dA);
                     sums.add(v, 2 * (s - s2), lane);
                 }
-                const int which = lane & 1, state = n0 + s2 + ((lane >> 1) & 1);  // what instruction lane%4 summed
+                const int which = lane & 1, state = state_of(s2 + ((lane >> 1) & 1));  // what instruction lane%4 summed
                 sums.finish(lane, [&](int token, float sum) { sh.part[warp][token][which][state] = sum; });
             }
             sum_parts<SPLIT>(du, part);
@@ -297,7 +317,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
         }
     }
     for (int k = 0; k < NS; ++k)
-        if (n0 + k < N) store_two<float>(pa + (size_t)(n0 + k) * c.channels, sh.dA[k][tid], me, ok.state);
+        if (state_of(k) < N) store_two<float>(pa + (size_t)state_of(k) * c.channels, sh.dA[k][tid], me, ok.state);
 #pragma unroll
     for (int o = PAIRS; o < 32; o *= 2) {
         dD = add2(dD, make_float2(__shfl_xor_sync(0xffffffffu, dD.x, o), __shfl_xor_sync(0xffffffffu, dD.y, o)));
@@ -317,13 +337,14 @@ __global__ void __launch_bounds__(SCAN_THREADS) sel_carry_kernel(SelCall c, Segm
     int i, first, lo, hi, end;
     if (!segment(c.seq, sg.seg, blockIdx.x, i, first, lo, hi, end) || lo == first) return;
     const Mine me = my_channels<NP>(c, blockIdx.y);
-    const int N = c.dstate, lane = threadIdx.x & 31, part = lane / PAIRS, pair = lane % PAIRS, n0 = part * NS;
+    const int N = c.dstate, lane = threadIdx.x & 31, part = lane / PAIRS, pair = lane % PAIRS;
+    auto state_of = [&](int k) { return k * SPLIT + part; };
     const T *B = static_cast<const T *>(c.B) + me.group * N, *C = static_cast<const T *>(c.C) + me.group * N;
     const T *dt = static_cast<const T *>(c.dt), *z = static_cast<const T *>(c.z), *dy = static_cast<const T *>(c.dy);
     float2 A2[NS], R[NS];
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
-        const int n = min(n0 + k, N - 1);
+        const int n = min(state_of(k), N - 1);
         A2[k] = make_float2(c.A[(size_t)me.c0 * N + n] * LOG2E, c.A[(size_t)me.c1 * N + n] * LOG2E);
         R[k] = make_float2(0.f, 0.f);
     }
@@ -353,11 +374,14 @@ __global__ void __launch_bounds__(SCAN_THREADS) sel_carry_kernel(SelCall c, Segm
             for (int k = GROUP - 1; k >= 0; --k) {
                 const int from = pair + k % SPLIT * PAIRS;
                 const float2 d2 = SPLIT == 1 ? dl[k / SPLIT] : shfl2(dl[k / SPLIT], from), e2 = SPLIT == 1 ? e[k / SPLIT] : shfl2(e[k / SPLIT], from);
+                const float most = fmaxf(fabsf(d2.x), fabsf(d2.y));
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
-                    const float4 v = bc[(t + k) * NP + n0 + s];
-                    const float2 arg = mul2(d2, A2[s]);
-                    R[s] = mul2(make_float2(ex2a(arg.x), ex2a(arg.y)), fma2(e2, make_float2(v.z, v.w), R[s]));
+                    const float4 v = bc[(t + k) * NP + state_of(s)];
+                    const float2 x = mul2(d2, A2[s]);
+                    const bool small = __all_sync(0xffffffffu, most * fmaxf(fabsf(A2[s].x), fabsf(A2[s].y)) <= SMALL_EXP);
+                    const float2 a = small ? ex2_small(x) : make_float2(ex2a(x.x), ex2a(x.y));
+                    R[s] = mul2(a, fma2(e2, make_float2(v.z, v.w), R[s]));
                 }
             }
         }
@@ -365,7 +389,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) sel_carry_kernel(SelCall c, Segm
     float *o = sg.state + (size_t)blockIdx.x * N * c.channels;
 #pragma unroll
     for (int k = 0; k < NS; ++k)
-        if (n0 + k < N) store_two<float>(o + (size_t)(n0 + k) * c.channels, R[k], me, ok.state);
+        if (state_of(k) < N) store_two<float>(o + (size_t)state_of(k) * c.channels, R[k], me, ok.state);
 #pragma unroll
     for (int k = PAIRS; k < 32; k *= 2)
         steps = add2(steps, make_float2(__shfl_xor_sync(0xffffffffu, steps.x, k), __shfl_xor_sync(0xffffffffu, steps.y, k)));
@@ -407,17 +431,17 @@ __global__ void __launch_bounds__(256) sel_bwd_sum(SelCall c, Parts parts, int s
     }
     const long long u = (long long)(blockIdx.x - row_blocks) * 256 + threadIdx.x, na = (long long)c.channels * N;
     if (u < na) {
-        float s = 0.f;
+        double s = 0.;
 #pragma unroll 8
         for (int i = 0; i < slots; ++i) s += parts.a[i * na + u];
-        c.dA[u % c.channels * N + u / c.channels] = s;
+        c.dA[u % c.channels * N + u / c.channels] = (float)s;
     } else if (u < na + 2 * c.channels) {
         const long long v = u - na;
-        float s = 0.f;
+        double s = 0.;
 #pragma unroll 8
         for (int i = 0; i < slots; ++i) s += parts.d[(size_t)i * 2 * c.channels + v];
         float *o = v < c.channels ? c.dD : c.dbias;
-        if (o) o[v < c.channels ? v : v - c.channels] = s;
+        if (o) o[v < c.channels ? v : v - c.channels] = (float)s;
     }
 }
 

@@ -4,7 +4,7 @@ their gradients, and the norms before and after the block.
 
 The functions have the C entry points' names (``include/ssd.h`` says what each
 argument means).  Their checks, outputs and scratch are in the native module _bind
-(``csrc/bind.cpp``), which makes the C calls: from Python they cost as much as the
+(``csrc/bind.cpp``), which makes the C calls: from Python they cost more than the
 launch of a small kernel itself.  Inputs that a
 projection's output holds side by side may be passed as slices: rows may be
 strided, the last dimension may not.  Outputs and scratch are allocated for each
@@ -156,7 +156,8 @@ def ssd_residual_rmsnorm(x, weight, residual=None, scale=None, *, eps=1e-5, out=
 def ssd_residual_rmsnorm_bwd(residual, weight, dout, dresidual=None, x=None, scale=None, *, eps=1e-5, out=None, stream=None):
     """Gradients of ssd_residual_rmsnorm from the r it returned: dict of dresidual (r's
     dtype), dx (dout's dtype; the same tensor where neither scale nor a wider dtype
-    sets them apart), dweight, and dscale (None without scale, which needs x)."""
+    sets them apart and ``out`` holds no dx), dweight, and dscale (None without scale,
+    which needs x).  ``out`` may pass them preallocated."""
     return _run("residual_rmsnorm_bwd", stream, residual, weight, dout, dresidual, x, scale, eps, out)
 
 
@@ -172,5 +173,6 @@ def ssd_gated_rmsnorm(y, z, weight, residual=None, scale=None, *, ngroups=1, nor
 def ssd_gated_rmsnorm_bwd(y, z, weight, dout, scale=None, *, ngroups=1, norm_before_gate=False, eps=1e-5, out=None,
                           stream=None):
     """Gradients of ssd_gated_rmsnorm: dict of dy, dz (None without z), dweight and
-    dscale (None without scale); the residual's gradient is dout."""
+    dscale (None without scale); the residual's gradient is dout.  ``out`` may pass them
+    preallocated."""
     return _run("gated_rmsnorm_bwd", stream, y, z, weight, dout, scale, ngroups, norm_before_gate, eps, out)

@@ -590,3 +590,124 @@ def test_given_outputs_are_used_and_checked():
     assert ssd.ssd_conv1d_varlen(empty, w[:, None].contiguous(), None, bounds([]))[0].shape == (0, d)
     none = ssd.ssd_conv1d_bwd(empty, w[:, None].contiguous(), None, bounds([]), empty)
     assert (none["dweight"] == 0).all()
+
+
+def test_gradients_into_given_tensors_and_in_place():
+    """A dx that the caller gives is filled even where it equals dresidual; dresidual may be
+    the upstream one, and the gated norm's result its residual."""
+    g, n, d = gen(72), 37, 512
+    x, w, dout, up = randn(g, n, d), 1 + randn(g, d, scale=0.1), randn(g, n, d), randn(g, n, d)
+    want = ssd.ssd_residual_rmsnorm_bwd(x, w, dout, up)
+    dx = torch.full_like(x, 7.0)
+    got = ssd.ssd_residual_rmsnorm_bwd(x, w, dout, up, out=dict(dx=dx))
+    assert got["dx"] is dx and torch.equal(dx, want["dx"]) and torch.equal(got["dresidual"], want["dresidual"])
+    again = ssd.ssd_residual_rmsnorm_bwd(x, w, dout, up, out=want)  # the dict of an earlier call
+    assert again is want and torch.equal(want["dx"], dx)
+    here = up.clone()
+    got = ssd.ssd_residual_rmsnorm_bwd(x, w, dout, here, out=dict(dresidual=here))
+    assert got["dresidual"] is here and torch.equal(here, dx) and torch.equal(got["dweight"], want["dweight"])
+    res = randn(g, n, d)
+    plain = ssd.ssd_gated_rmsnorm(x, dout, w, res, ngroups=2)
+    assert ssd.ssd_gated_rmsnorm(x, dout, w, res, ngroups=2, out=res) is res and torch.equal(res, plain)
+
+
+def test_tokens_and_norms_in_graphs():
+    """A captured step of single tokens, replayed, moves the states on as plain calls do; a
+    captured training step of the conv and the norms gives the bits of plain calls, on two
+    streams and replayed while plain calls run."""
+    g, b, d, N, K = gen(62), 5, 64, 16, 4
+    ct = d + 2 * N
+    w, cb, A, nw = randn(g, ct, K), randn(g, ct), -randn(g, d, N).abs(), 1 + randn(g, d, scale=0.1)
+    slots = torch.tensor([3, 0, -1, 5, 1], dtype=torch.int32).cuda()
+    tokens = [(randn(g, b, ct, io=torch.bfloat16), randn(g, b, d, io=torch.bfloat16), randn(g, b, d, io=torch.bfloat16)) for _ in range(6)]
+
+    def states():
+        return torch.zeros(6, ct, K - 1, device="cuda", dtype=torch.bfloat16), torch.zeros(6, d, N, device="cuda")
+
+    def token(xbc, dt, z, conv_state, state):
+        x, B, C = ssd.ssd_conv1d_update(conv_state, xbc, w, cb, slots=slots, x_channels=d, bc_channels=N)
+        y = ssd.ssd_selective_state_update(state, x, dt, A, B.view(b, 1, N), C.view(b, 1, N), z=z, slots=slots)
+        return ssd.ssd_gated_rmsnorm(y, z, nw)
+
+    keep = [i for i in range(b) if i != 2]  # the skipped row's result is not written
+    plain = states()
+    want = [token(*t, *plain)[keep] for t in tokens]
+    mine, held = states(), [t.clone() for t in tokens[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = token(*held, *mine)
+    for t, r in zip(tokens, want):
+        for a, v in zip(held, t):
+            a.copy_(v)
+        graph.replay()
+        assert torch.equal(out[keep], r)
+    assert all(torch.equal(a, v) for a, v in zip(mine, plain))
+
+    cu, n = bounds([700, 1, 0, 323]), 1024
+    xbc, z, dy, r0 = randn(g, n, ct), randn(g, n, d), randn(g, n, d), randn(g, n, d)
+    dB = randn(g, n, N)
+
+    def step(**kw):
+        x, B, C = ssd.ssd_conv1d_varlen(xbc, w, cb, cu, x_channels=d, bc_channels=N, **kw)
+        h, r = ssd.ssd_residual_rmsnorm(x, nw, r0, nw, **kw)
+        o = ssd.ssd_gated_rmsnorm(h, z, nw, **kw)
+        go = ssd.ssd_gated_rmsnorm_bwd(h, z, nw, dy, **kw)
+        gr = ssd.ssd_residual_rmsnorm_bwd(r, nw, go["dy"], None, x, nw, **kw)
+        gc = ssd.ssd_conv1d_bwd(xbc, w, cb, cu, gr["dx"], dB, dB, **kw)
+        return [x, B, C, h, r, o] + [v for q in (go, gr, gc) for v in q.values() if v is not None]
+
+    want = step()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = [step(stream=st) for st in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, v) for q in got for a, v in zip(want, q))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for _ in range(3):
+        with torch.cuda.stream(streams[0]):
+            graph.replay()
+        got = step(stream=streams[1])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, v) and torch.equal(a, u) for a, v, u in zip(want, got, outs))
+    ssd.ssd_get_device_status()
+
+
+def test_offsets_past_32_bits():
+    """Rows and state slots that lie past 2^31 elements give the bits of small copies."""
+    g, d, N, rows = gen(63), 256, 64, 18
+    ld = (1 << 27) + 64
+    big = torch.empty(rows, ld, device="cuda", dtype=torch.bfloat16)
+    assert (rows - 1) * ld > 1 << 31
+    part = big[:, :3 * d + 2 * N]
+    part.copy_(randn(g, rows, 3 * d + 2 * N))
+    small = part.contiguous()
+
+    def cut(t):
+        return t[:, :d], t[:, d:2 * d], t[:, 2 * d:3 * d], t[:, 3 * d:3 * d + N].view(rows, 1, N), t[:, 3 * d + N:].view(rows, 1, N)
+
+    A, w = -randn(g, d, N).abs(), randn(g, d, 4)
+    nw, cu, slots = 1 + randn(g, d, scale=0.1), bounds([7, rows - 7]), (1 << 17) + 4
+    state, few = torch.empty(slots, d, N, device="cuda"), torch.zeros(3, d, N, device="cuda")
+    assert (slots - 3) * d * N > 1 << 31
+    state[-3:].zero_()
+    far, near = torch.tensor([slots - 1, slots - 3], dtype=torch.int32).cuda(), torch.tensor([2, 0], dtype=torch.int32).cuda()
+    dy = randn(g, rows, d, io=torch.bfloat16)
+    got = []
+    for t, st, sl in ((part, state, far), (small, few, near)):
+        x, dt, z, B, C = cut(t)
+        y, kept = ssd.ssd_selective_scan_varlen(x, dt, A, B, C, cu, z=z, state=st, slots=sl, return_chunk_states=True)
+        grads = ssd.ssd_selective_scan_bwd(x, dt, A, B, C, cu, dy, kept, z=z)
+        first = [v[:2] for v in (x, dt, B, C, z)]
+        tok = ssd.ssd_selective_state_update(st, first[0], first[1], A, first[2], first[3], z=first[4], slots=sl)
+        conv = ssd.ssd_conv1d_varlen(x, w, None, cu)[0]
+        gc = ssd.ssd_conv1d_bwd(x, w, None, cu, dy)
+        norm, r = ssd.ssd_residual_rmsnorm(x, nw, z)
+        gn = ssd.ssd_gated_rmsnorm_bwd(x, z, nw, dy)
+        gr = ssd.ssd_residual_rmsnorm_bwd(x, nw, dy)
+        got.append([y, tok, conv, norm, r, ssd.ssd_gated_rmsnorm(x, z, nw), st[-3:]]
+                   + [v for q in (grads, gc, gn, gr) for v in q.values() if v is not None])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    ssd.ssd_get_device_status()
