@@ -302,7 +302,10 @@ __global__ void __launch_bounds__(UPD_THREADS) sel_update_kernel(SelCall c, bool
     }
 }
 
-constexpr int FWD_WARPS_PER_SM = 16;
+constexpr int FWD_WARPS_PER_SM = 32;
+inline int fwd_seg(int tokens, int nseq, int channels, int N) {
+    return choose_seg(tokens, nseq, channels, N <= 8 ? 32 : N <= 16 ? 16 : N <= 32 ? 8 : 4, FWD_WARPS_PER_SM);  // as FwdLanes
+}
 
 template <typename T, int NP, bool FULL> cudaError_t run_pass(const SelCall &c, const Segments &sg, cudaStream_t st) {
     constexpr int CH = FwdLanes<NP>::CH;
@@ -350,13 +353,13 @@ cudaError_t launch_sel_join(const SelCall &c, const Segments &s, bool backwards,
 }
 
 size_t sel_fwd_workspace(int tokens, int nseq, int channels, int dstate) {
-    const int seg = choose_seg(tokens, nseq, channels, FWD_WARPS_PER_SM);
+    const int seg = fwd_seg(tokens, nseq, channels, dstate);
     return seg == WHOLE ? 0 : (size_t)seg_slots(tokens, nseq, seg) * channels * (dstate + 1) * sizeof(float);
 }
 
 cudaError_t launch_sel_varlen(const SelCall &c, float *ws, cudaStream_t st) {
     Segments sg;
-    sg.seg = choose_seg(c.seq.tokens, c.seq.nseq, c.channels, FWD_WARPS_PER_SM);
+    sg.seg = fwd_seg(c.seq.tokens, c.seq.nseq, c.channels, c.dstate);
     sg.slots = seg_slots(c.seq.tokens, c.seq.nseq, sg.seg);
     sg.state = ws, sg.steps = ws + (sg.seg == WHOLE ? 0 : (size_t)sg.slots * c.dstate * c.channels);
     return c.bf16 ? run_fwd<__nv_bfloat16>(c, sg, st) : run_fwd<float>(c, sg, st);

@@ -145,10 +145,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
     for (int chunk = c_last; chunk >= c_first; --chunk) {
         const int t0 = first + chunk * SEL_CHUNK, n = min(SEL_CHUNK, hi - t0);
         __syncthreads();  // the chunk before has been read
-        fetch_rows<T, CH>(sh.x, static_cast<const T *>(c.x) + t0 * c.ld_x + t_first, c.ld_x, n, t_cols, ok.wide);
-        fetch_rows<T, CH>(sh.dt, static_cast<const T *>(c.dt) + t0 * c.ld_dt + t_first, c.ld_dt, n, t_cols, ok.wide);
-        if (c.z) fetch_rows<T, CH>(sh.z, static_cast<const T *>(c.z) + t0 * c.ld_z + t_first, c.ld_z, n, t_cols, ok.wide);
-        fetch_rows<T, CH>(sh.dy, static_cast<const T *>(c.dy) + (size_t)t0 * c.channels + t_first, c.channels, n, t_cols, ok.wide);
+        const RowsOf<T, CH> rows[4] = {{sh.x, static_cast<const T *>(c.x) + t0 * c.ld_x + t_first, c.ld_x},
+                                       {sh.dt, static_cast<const T *>(c.dt) + t0 * c.ld_dt + t_first, c.ld_dt},
+                                       {sh.dy, static_cast<const T *>(c.dy) + (size_t)t0 * c.channels + t_first, c.channels},
+                                       {sh.z, static_cast<const T *>(c.z) + (c.z ? t0 * c.ld_z + t_first : 0), c.ld_z}};
+        fetch_rows(rows, c.z ? 4 : 3, n, t_cols, ok.wide, ok.paired);
 #pragma unroll
         for (int k = 0; k < NS; ++k) {
             if (state_of(k) >= N) continue;
@@ -350,39 +351,73 @@ __global__ void __launch_bounds__(SCAN_THREADS) sel_carry_kernel(SelCall c, Segm
     }
     const float2 bias = c.dt_bias ? make_float2(c.dt_bias[me.c0], c.dt_bias[me.c1]) : make_float2(0.f, 0.f);
     float2 steps = make_float2(0.f, 0.f);
-    for (int t0 = lo + (hi - 1 - lo) / SEL_CHUNK * SEL_CHUNK; t0 >= lo; t0 -= SEL_CHUNK) {
-        const int n = min(SEL_CHUNK, hi - t0);
-        Stage stage;
-        stage.load(B + t0 * c.ld_b, c.ld_b, C + t0 * c.ld_c, c.ld_c, n, N, ok.bc);
-        __syncthreads();
-        stage.put(bc);
-        __syncthreads();
-#pragma unroll 1
-        for (int t = (n - 1) / GROUP * GROUP; t >= 0; t -= GROUP) {
-            float2 dl[OWN], e[OWN];
+    // A group of tokens at a time, the next one's rows and the next chunk's B and C on their
+    // way (without, the kernel took 216 us, 91 us so, for 5925 tokens of 1658
+    // channels of 4 states).
+    Two<T> nd[OWN], ny[OWN], nz[OWN];
+    auto fetch = [&](int g) {
 #pragma unroll
-            for (int j = 0; j < OWN; ++j) {
-                const int at = t + j * SPLIT + part, row = t0 + min(at, n - 1);
-                dl[j] = add2(load_two(dt + row * c.ld_dt, me, ok.paired).f(), bias);
-                e[j] = load_two(dy + (size_t)row * c.channels, me, ok.paired).f();
-                if (c.softplus) dl[j] = softplus2(dl[j]);
-                if (c.z) e[j] = mul2(e[j], silu2(load_two(z + row * c.ld_z, me, ok.paired).f()));
-                if (at >= n) dl[j] = e[j] = make_float2(0.f, 0.f);
-                steps = add2(steps, dl[j]);
+        for (int j = 0; j < OWN; ++j) {
+            const int row = min(lo + g * GROUP + j * SPLIT + part, hi - 1);
+            nd[j] = load_two(dt + row * c.ld_dt, me, ok.paired);
+            ny[j] = load_two(dy + (size_t)row * c.channels, me, ok.paired);
+            if (c.z) nz[j] = load_two(z + row * c.ld_z, me, ok.paired);
+        }
+    };
+    Stage stage;
+    auto load_bc = [&](int chunk) {
+        const int t0 = lo + chunk * SEL_CHUNK;
+        stage.load(B + t0 * c.ld_b, c.ld_b, C + t0 * c.ld_c, c.ld_c, min(SEL_CHUNK, hi - t0), N, ok.bc);
+    };
+    constexpr int GROUPS = SEL_CHUNK / GROUP;
+    const int last = (hi - 1 - lo) / GROUP;
+    load_bc(last / GROUPS);
+    fetch(last);
+#pragma unroll 1
+    for (int g = last, staged = -1; g >= 0; --g) {
+        if (g / GROUPS != staged) {
+            staged = g / GROUPS;
+            __syncthreads();  // the chunk behind has been read
+            stage.put(bc);
+            __syncthreads();
+            if (staged > 0) load_bc(staged - 1);
+        }
+        float2 dl[OWN], e[OWN], d2[GROUP], e2[GROUP];
+        float most = 0.f;
+#pragma unroll
+        for (int j = 0; j < OWN; ++j) {
+            dl[j] = add2(nd[j].f(), bias);
+            e[j] = ny[j].f();
+            if (c.softplus) dl[j] = softplus2(dl[j]);
+            if (c.z) e[j] = mul2(e[j], silu2(nz[j].f()));
+            if (lo + g * GROUP + j * SPLIT + part >= hi) dl[j] = e[j] = make_float2(0.f, 0.f);
+            steps = add2(steps, dl[j]);
+        }
+        if (g > 0) fetch(g - 1);
+#pragma unroll
+        for (int k = 0; k < GROUP; ++k) {
+            const int from = pair + k % SPLIT * PAIRS;
+            d2[k] = SPLIT == 1 ? dl[k / SPLIT] : shfl2(dl[k / SPLIT], from);
+            e2[k] = SPLIT == 1 ? e[k / SPLIT] : shfl2(e[k / SPLIT], from);
+            most = fmaxf(most, fmaxf(fabsf(d2[k].x), fabsf(d2[k].y)));
+        }
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            float2 a[GROUP];
+            if (__all_sync(0xffffffffu, most * fmaxf(fabsf(A2[s].x), fabsf(A2[s].y)) <= SMALL_EXP)) {
+#pragma unroll
+                for (int k = 0; k < GROUP; ++k) a[k] = ex2_small(mul2(d2[k], A2[s]));
+            } else {
+#pragma unroll
+                for (int k = 0; k < GROUP; ++k) {
+                    const float2 x = mul2(d2[k], A2[s]);
+                    a[k] = make_float2(ex2a(x.x), ex2a(x.y));
+                }
             }
 #pragma unroll
             for (int k = GROUP - 1; k >= 0; --k) {
-                const int from = pair + k % SPLIT * PAIRS;
-                const float2 d2 = SPLIT == 1 ? dl[k / SPLIT] : shfl2(dl[k / SPLIT], from), e2 = SPLIT == 1 ? e[k / SPLIT] : shfl2(e[k / SPLIT], from);
-                const float most = fmaxf(fabsf(d2.x), fabsf(d2.y));
-#pragma unroll
-                for (int s = 0; s < NS; ++s) {
-                    const float4 v = bc[(t + k) * NP + state_of(s)];
-                    const float2 x = mul2(d2, A2[s]);
-                    const bool small = __all_sync(0xffffffffu, most * fmaxf(fabsf(A2[s].x), fabsf(A2[s].y)) <= SMALL_EXP);
-                    const float2 a = small ? ex2_small(x) : make_float2(ex2a(x.x), ex2a(x.y));
-                    R[s] = mul2(a, fma2(e2, make_float2(v.z, v.w), R[s]));
-                }
+                const float4 v = bc[(g % GROUPS * GROUP + k) * NP + state_of(s)];
+                R[s] = mul2(a[k], fma2(e2[k], make_float2(v.z, v.w), R[s]));
             }
         }
     }
@@ -445,15 +480,17 @@ __global__ void __launch_bounds__(256) sel_bwd_sum(SelCall c, Parts parts, int s
     }
 }
 
-constexpr int BWD_WARPS_PER_SM = 12;
+// Warps counted as of 32 channels (64 of up to 8 states): counting the 16 that 32 and 64
+// states have cuts less, and took 6 to 12 % more at 4096 tokens of 1024 channels.
+constexpr int BWD_WARPS_PER_SM = 16;
 
 struct Layout {  // of the workspace, in floats
     int seg, slots, tiles;
     size_t bc, a, d, carried, steps, total;
     Layout(int tokens, int nseq, int channels, int groups, int N) {
-        seg = choose_seg(tokens, nseq, channels, BWD_WARPS_PER_SM);
-        slots = tokens > 0 ? seg_slots(tokens, nseq, seg) : 0;
         const int split = N <= 8 ? 1 : N <= 16 ? 2 : 4, ch = 2 * SCAN_THREADS / split;  // as Lanes
+        seg = choose_seg(tokens, nseq, channels, split == 1 ? 64 : 32, BWD_WARPS_PER_SM);
+        slots = tokens > 0 ? seg_slots(tokens, nseq, seg) : 0;
         tiles = (channels / groups + ch - 1) / ch;
         bc = 0;
         a = bc + (size_t)groups * tiles * tokens * 2 * N;

@@ -30,14 +30,16 @@ struct Segments {
 
 inline int seg_slots(int tokens, int nseq, int seg) { return seg == WHOLE ? nseq : tokens / seg + nseq; }
 
-// The cut: none once there are `warps_per_sm` warps for each SM, else segments so
-// short that there are, but of 64 tokens at least (a multiple of 16, so that kept
-// states fall on segment starts).
-inline int choose_seg(int tokens, int nseq, int channels, int warps_per_sm) {
-    const long long want = 148LL * warps_per_sm, per_token = (channels + 31) / 32;
+// The cut, of `per_warp` channels to a warp: none once there are half of `warps_per_sm`
+// warps for each SM, else segments so short that there are all, but of 32 tokens at least
+// (a multiple of 16, so that kept states fall on segment starts).  8 x 256 tokens of 256
+// channels, forward and gradient, 16 states: 159 us with 64 at least, 105 us with 32, 87 us
+// with 16, which takes 8 % more for one sequence of 4096 tokens.
+inline int choose_seg(int tokens, int nseq, int channels, int per_warp, int warps_per_sm) {
+    const long long want = 148LL * warps_per_sm, per_token = (channels + per_warp - 1) / per_warp;
     if (nseq * per_token * 2 >= want) return WHOLE;
     const long long seg = (tokens * per_token / want + 15) / 16 * 16;
-    return seg < 64 ? 64 : (int)seg;
+    return seg < 32 ? 32 : (int)seg;
 }
 
 // What slot s stands for: false when it is no segment.
@@ -83,20 +85,55 @@ __device__ __forceinline__ void cp4(void *smem, const void *gmem) {
 }
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// n rows of `cols` channels into tile[..][CH]; wide: aligned 16-byte pieces, which
-// land by cp_wait_all, else plain copies.
-template <typename T, int CH>
-__device__ __forceinline__ void fetch_rows(T (*to)[CH], const T *src, long long ld, int n, int cols, bool wide) {
-    constexpr int E = 16 / (int)sizeof(T), PER = CH / E;
-    if (wide) {
+// n rows of `cols` channels of K tensors into their tiles [..][CH]: by asynchronous copies
+// of 16 or 4 bytes where rows divide into them (they land by cp_wait_all), else through
+// registers, four rows' elements of all tensors on their way at a time.  (An element at a
+// time through registers, 19 sequences of 753 tokens, 1565 channels of 8 states in float32
+// took 366 us, 203 us so.)
+template <typename T, int CH> struct RowsOf {
+    T (*to)[CH];
+    const T *src;
+    long long ld;
+};
+template <int BYTES, typename T, int CH, int K>
+__device__ __forceinline__ void copy_rows(const RowsOf<T, CH> (&a)[K], int used, int n, int cols) {
+    constexpr int E = BYTES / (int)sizeof(T), PER = CH / E;
+#pragma unroll
+    for (int q = 0; q < K; ++q) {
+        if (q >= used) break;
+#pragma unroll 2
         for (int u = threadIdx.x; u < n * PER; u += SCAN_THREADS) {
             const int r = u / PER, k = u % PER * E;
-            if (k < cols) cp16(&to[r][k], src + r * ld + k);
+            if (k >= cols) continue;
+            if constexpr (BYTES == 16) cp16(&a[q].to[r][k], a[q].src + r * a[q].ld + k);
+            if constexpr (BYTES == 4) cp4(&a[q].to[r][k], a[q].src + r * a[q].ld + k);
         }
+    }
+}
+template <typename T, int CH, int K>
+__device__ __forceinline__ void fetch_rows(const RowsOf<T, CH> (&a)[K], int used, int n, int cols, bool wide, bool paired) {
+    if (wide) {
+        copy_rows<16>(a, used, n, cols);
+    } else if (sizeof(T) == 4 || paired) {
+        copy_rows<4>(a, used, n, cols);
     } else {
-        for (int u = threadIdx.x; u < n * CH; u += SCAN_THREADS) {
-            const int r = u / CH, k = u % CH;
-            if (k < cols) to[r][k] = src[r * ld + k];
+        constexpr int U = 2;
+        for (int u0 = threadIdx.x; u0 < n * CH; u0 += U * SCAN_THREADS) {
+            T v[K][U];
+#pragma unroll
+            for (int q = 0; q < K; ++q)
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const int u = u0 + j * SCAN_THREADS, r = u / CH, k = u % CH;
+                    if (q < used && r < n && k < cols) v[q][j] = a[q].src[r * a[q].ld + k];
+                }
+#pragma unroll
+            for (int q = 0; q < K; ++q)
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const int u = u0 + j * SCAN_THREADS, r = u / CH, k = u % CH;
+                    if (q < used && r < n && k < cols) a[q].to[r][k] = v[q][j];
+                }
         }
     }
 }
