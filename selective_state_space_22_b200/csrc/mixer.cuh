@@ -160,6 +160,9 @@ template <typename T, int V, bool WIDE> __device__ __forceinline__ void load_v(c
         const uint2 q = *reinterpret_cast<const uint2 *>(p);
         v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
         v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
+    } else if constexpr (WIDE && sizeof(T) == 2 && V == 2) {
+        const uint32_t q = *reinterpret_cast<const uint32_t *>(p);
+        v[0] = __uint_as_float(q << 16), v[1] = __uint_as_float(q & 0xffff0000u);
     } else if constexpr (WIDE && sizeof(T) == 4 && V == 2) {
         const float2 q = *reinterpret_cast<const float2 *>(p);
         v[0] = q.x, v[1] = q.y;
@@ -184,6 +187,8 @@ template <typename T, int V, bool WIDE> __device__ __forceinline__ void store_v(
             make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     } else if constexpr (WIDE && sizeof(T) == 2 && V == 4) {
         *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    } else if constexpr (WIDE && sizeof(T) == 2 && V == 2) {
+        *reinterpret_cast<uint32_t *>(p) = pack_bf16(v[0], v[1]);
     } else if constexpr (WIDE && sizeof(T) == 4 && V == 2) {
         *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
     } else if constexpr (WIDE && sizeof(T) == 4 && V % 4 == 0) {

@@ -404,11 +404,12 @@ __global__ void __launch_bounds__(1024) norm_bwd_sum(const float *__restrict__ p
 }
 
 // Calls f with the unit's split: TPR threads (a power of two, MIN .. 512) of VPT
-// vectors of V channels; four (then 16) single channels where rows are not aligned
-// vectors.  Forwards a thread takes two vectors once there are enough units (up to 512
-// bf16 channels then stay in one warp: 8192 x 8 groups of 512 take 42.3 us, 49.6 us with
-// one vector; eight rows of 2048 4.6 us, 4.0 us with one).  Backwards it takes one where
-// 512 threads reach (with two the same groups took 118 us, 101 us with one).
+// vectors of V channels.  Forwards a thread takes two vectors of 16 bytes once there are
+// enough units (up to 512 bf16 channels then stay in one warp: 8192 x 8 groups of 512 take
+// 42.3 us, 49.6 us with one vector; eight rows of 2048 4.6 us, 4.0 us with one), and eight
+// single channels where four would take more than a warp (5175 x 1333 24.5 us, 30.7 us with
+// four; 20000 x 90 14.3 us, 10.2 us with four).  Backwards it takes one vector of 16 bytes
+// where 512 threads reach (with two the same groups took 118 us, 101 us with one).
 template <int VPT, int MIN, typename F> cudaError_t with_tpr(int vectors, F &&f) {
     const int need = (vectors + VPT - 1) / VPT;
     constexpr std::integral_constant<int, VPT> vpt{};
@@ -425,8 +426,13 @@ template <int VPT, int MIN, typename F> cudaError_t with_tpr(int vectors, F &&f)
 template <int V, typename F> cudaError_t with_split(int width, bool two, F &&f) {
     static_assert(NORM_MAX_WIDTH == 8192, "the splits below end there");
     const int vectors = (width + V - 1) / V;
-    if constexpr (V == 1) {
-        return vectors <= 2048 ? with_tpr<4, 32>(vectors, f) : with_tpr<16, 256>(vectors, f);
+    if constexpr (V <= 2) {
+        if constexpr (V == 1) {
+            if (vectors > 4096) return with_tpr<16, 512>(vectors, f);
+            if (two && vectors > 128 && vectors <= 2048) return with_tpr<8, 32>(vectors, f);
+        }
+        if (vectors <= 2048) return with_tpr<4, 32>(vectors, f);
+        return with_tpr<8, 512>(vectors, f);
     } else {
         if (vectors <= (two ? 32 : 512)) return with_tpr<1, 32>(vectors, f);
         if constexpr (V == 4)
@@ -476,40 +482,53 @@ template <typename T, int V> cudaError_t run_after_bwd(const NormCall &c, float 
     });
 }
 
-// Whether every row (and group) can be read as vectors of V channels; `V` floats
-// are read as 16-byte accesses, so 16-byte alignment serves every type.
+// Whether every row (and group) can be read as vectors of V channels, at most 16 bytes an
+// access.
 bool wide_rows(const NormCall &c, int V) {
     const size_t e = c.bf16 ? 2 : 4, er = c.res_bf16 ? 2 : 4;
-    return c.width % V == 0 && (c.width / c.groups) % V == 0 && (!c.x || rows_aligned(c.x, c.ld_x, e, 16)) &&
-           (!c.z || rows_aligned(c.z, c.ld_z, e, 16)) && (!c.res || rows_aligned(c.res, c.ld_res, er, 16));
+    return c.width % V == 0 && (c.width / c.groups) % V == 0 && (!c.x || rows_aligned(c.x, c.ld_x, e, min(16, V * (int)e))) &&
+           (!c.z || rows_aligned(c.z, c.ld_z, e, min(16, V * (int)e))) && (!c.res || rows_aligned(c.res, c.ld_res, er, min(16, V * (int)er)));
+}
+
+// Calls f with the channels of a vector: 16 bytes of the io type, pairs, or single ones
+// (bf16, norm after: 5175 x 1332 channels in pairs 20 us and 42 us backwards, single 31 and
+// 66; 8192 x 4004 82 and 212, single 170 and 647).  Backwards up to 512 channels stay single:
+// 8192 x 8 groups of 500 take 166 us so and 199 us in pairs.
+template <typename F> cudaError_t with_vectors(const NormCall &c, bool backward, F &&f) {
+    if (wide_rows(c, c.bf16 ? 8 : 4)) return f(std::integral_constant<int, 8>{});
+    if (wide_rows(c, 2) && (!backward || c.width / c.groups > 512)) return f(std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, 1>{});
+}
+// .. and with the types of the io and the residual.
+template <typename F> cudaError_t with_types(const NormCall &c, bool backward, F &&f) {
+    using H = __nv_bfloat16;
+    return with_vectors(c, backward, [&](auto v) {
+        constexpr std::integral_constant<int, (v() > 4 ? 4 : v())> v4{};
+        if (!c.bf16) return f(float(), float(), v4);
+        return c.res_bf16 ? f(H(), H(), v) : f(H(), float(), v);
+    });
 }
 
 }  // namespace
 
 cudaError_t launch_norm_before(const NormCall &c, cudaStream_t st) {
-    using H = __nv_bfloat16;
-    if (!c.bf16) return wide_rows(c, 4) ? run_before<float, float, 4>(c, st) : run_before<float, float, 1>(c, st);
-    if (c.res_bf16) return wide_rows(c, 8) ? run_before<H, H, 8>(c, st) : run_before<H, H, 1>(c, st);
-    return wide_rows(c, 8) ? run_before<H, float, 8>(c, st) : run_before<H, float, 1>(c, st);
+    return with_types(c, false, [&](auto t, auto r, auto v) { return run_before<decltype(t), decltype(r), v()>(c, st); });
 }
 cudaError_t launch_norm_after(const NormCall &c, cudaStream_t st) {
-    using H = __nv_bfloat16;
-    if (!c.bf16) return wide_rows(c, 4) ? run_after<float, 4>(c, st) : run_after<float, 1>(c, st);
-    return wide_rows(c, 8) ? run_after<H, 8>(c, st) : run_after<H, 1>(c, st);
+    return with_types(c, false, [&](auto t, auto r, auto v) {
+        return std::is_same<decltype(t), decltype(r)>::value ? run_after<decltype(t), v()>(c, st) : cudaErrorInvalidValue;
+    });
 }
 size_t norm_bwd_workspace(int rows, int width) {  // blocks have 128 threads at least
     return 2 * (size_t)min(rows, 2 * BWD_BLOCKS) * width * sizeof(float);
 }
 cudaError_t launch_norm_before_bwd(const NormCall &c, float *ws, cudaStream_t st) {
-    using H = __nv_bfloat16;
-    if (!c.bf16) return wide_rows(c, 4) ? run_before_bwd<float, float, 4>(c, ws, st) : run_before_bwd<float, float, 1>(c, ws, st);
-    if (c.res_bf16) return wide_rows(c, 8) ? run_before_bwd<H, H, 8>(c, ws, st) : run_before_bwd<H, H, 1>(c, ws, st);
-    return wide_rows(c, 8) ? run_before_bwd<H, float, 8>(c, ws, st) : run_before_bwd<H, float, 1>(c, ws, st);
+    return with_types(c, true, [&](auto t, auto r, auto v) { return run_before_bwd<decltype(t), decltype(r), v()>(c, ws, st); });
 }
 cudaError_t launch_norm_after_bwd(const NormCall &c, float *ws, cudaStream_t st) {
-    using H = __nv_bfloat16;
-    if (!c.bf16) return wide_rows(c, 4) ? run_after_bwd<float, 4>(c, ws, st) : run_after_bwd<float, 1>(c, ws, st);
-    return wide_rows(c, 8) ? run_after_bwd<H, 8>(c, ws, st) : run_after_bwd<H, 1>(c, ws, st);
+    return with_types(c, true, [&](auto t, auto r, auto v) {
+        return std::is_same<decltype(t), decltype(r)>::value ? run_after_bwd<decltype(t), v()>(c, ws, st) : cudaErrorInvalidValue;
+    });
 }
 
 }  // namespace ssd
