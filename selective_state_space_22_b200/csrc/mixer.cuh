@@ -62,6 +62,9 @@ __device__ __forceinline__ float ex2a(float v) {  // 2^v, relative error about 2
     return r;
 }
 constexpr float LOG2E = 1.4426950408889634f;
+// A in powers of two, and finite: a step of nothing (a token past the end) is a decay of
+// one then, and any other of zero, also where A is -infinity.
+__device__ __forceinline__ float rate(float A) { return fabsf(A) <= 1e38f ? A * LOG2E : A < 0.f ? -3e38f : A; }
 
 __device__ __forceinline__ float rcpa(float v) {  // 1/v, 1 ulp; subnormal results are zero
     float r;

@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, FWD_BLOCKS_PER_SM) sel_fwd_kerne
         if (FULL && sg.seg != WHOLE) return carried[(size_t)n * c.channels];
         return init ? state[n] : 0.f;
     };
-    auto load_A = [&](int n) { return n < N ? c.A[(size_t)d * N + n] * LOG2E : 0.f; };
+    auto load_A = [&](int n) { return n < N ? rate(c.A[(size_t)d * N + n]) : 0.f; };
     float2 A2[P], h[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(128) sel_join_kernel(SelCall c, Segments sg, b
     if (!seq_rows(c.seq, i, lo, hi) || lo == hi) return;
     const int slot = !backwards && c.state ? slot_of(c.seq.slots, c.seq.nslots, i, c.seq.dev_error) : -1;
     if (d >= c.channels) return;
-    const float A2 = c.A[(size_t)d * N + n] * LOG2E;
+    const float A2 = rate(c.A[(size_t)d * N + n]);
     float h = slot >= 0 && c.seq.has_init && c.seq.has_init[i] ? c.state[((size_t)slot * c.channels + d) * N + n] : 0.f;
     const int count = (hi - lo + sg.seg - 1) / sg.seg, s0 = lo / sg.seg + i;
     const size_t step = (size_t)N * c.channels;

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
         const int n = state_of(k);
         float2 A2 = zero, G = zero;
         if (n < N) {
-            A2 = make_float2(c.A[(size_t)me.c0 * N + n] * LOG2E, c.A[(size_t)me.c1 * N + n] * LOG2E);
+            A2 = make_float2(rate(c.A[(size_t)me.c0 * N + n]), rate(c.A[(size_t)me.c1 * N + n]));
             const float *from = sg.state + blockIdx.x * step + (size_t)n * c.channels;
             if (sg.seg != WHOLE) G = make_float2(from[me.c0], from[me.c1]);
         }
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) sel_carry_kernel(SelCall c, Segm
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
         const int n = min(state_of(k), N - 1);
-        A2[k] = make_float2(c.A[(size_t)me.c0 * N + n] * LOG2E, c.A[(size_t)me.c1 * N + n] * LOG2E);
+        A2[k] = make_float2(rate(c.A[(size_t)me.c0 * N + n]), rate(c.A[(size_t)me.c1 * N + n]));
         R[k] = make_float2(0.f, 0.f);
     }
     const float2 bias = c.dt_bias ? make_float2(c.dt_bias[me.c0], c.dt_bias[me.c1]) : make_float2(0.f, 0.f);

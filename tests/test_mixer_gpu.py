@@ -711,3 +711,27 @@ def test_offsets_past_32_bits():
                    + [v for q in (grads, gc, gn, gr) for v in q.values() if v is not None])
     assert all(torch.equal(a, b) for a, b in zip(*got))
     ssd.ssd_get_device_status()
+
+
+@pytest.mark.parametrize("lens", [[5], [3, 12, 1], [700]])
+@pytest.mark.parametrize("N", [4, 16, 64])
+def test_states_that_forget_everything(lens, N):
+    """A = -infinity (and one whose product with a step leaves float32): such a state holds its
+    last input alone, whatever the sequence's length, and hands no gradient back."""
+    g, n, d = gen(73), sum(lens), 34
+    (x, dt, A, B, C), opt = sel_inputs(g, n, d, 1, N, torch.float32, 0)
+    A[:, 1], A[3, 2] = -float("inf"), -3e38
+    cu, state = bounds(lens), torch.zeros(len(lens), d, N, device="cuda")
+    y, kept = ssd.ssd_selective_scan_varlen(x, dt, A, B, C, cu, *opt, state=state, return_chunk_states=True)
+    grads = ssd.ssd_selective_scan_bwd(x, dt, A, B, C, cu, torch.ones_like(y), kept, *opt)
+    assert all(torch.isfinite(v).all() for v in [y, state, *grads.values()])
+    assert (grads["dA"][:, 1] == 0).all() and grads["dA"][3, 2] == 0
+    last = cu[1:].long() - 1
+    delta = torch.nn.functional.softplus((dt[last] + opt[2]).double())
+    want = delta * x[last].double() * B[last, 0, 1:2].double()
+    # softplus and its approximate exponential (as in the scans' other tests: 64 roundings), two products
+    assert ((state[:, :, 1].double() - want).abs() <= 66 * 2.0 ** -24 * want.abs()).all()
+    mild = A.clamp(min=-1e4)  # exp(-1e4 step) is zero in float32 too, for steps above 0.011
+    if (torch.nn.functional.softplus(dt + opt[2]) > 0.011).all():
+        assert torch.equal(y, ssd.ssd_selective_scan_varlen(x, dt, mild, B, C, cu, *opt)[0])
+    ssd.ssd_get_device_status()
