@@ -224,12 +224,13 @@ __global__ void __launch_bounds__(128) sel_join_kernel(SelCall c, Segments sg, b
 // that a group reads and writes whole rows of the state, all loads first, and a lane
 // ends with its own channel's readout.  (LP lanes doing the scalar work of each of
 // their channels together measured 43.6 us against 27.5 us for 256 x 4096 channels
-// of 16 states: five times the instructions.)  LP = 0: any dstate, a lane per channel.
+// of 16 states: five times the instructions; 64 registers, so that eight blocks are on an
+// SM, 26.1 us, 48 31.7 us.)  LP = 0: any dstate, a lane per channel.
 // SAME: the warp's channels lie in one B/C group.  Bound by HBM: the state in and out
-// (27.5 us is 5.2 TB/s of the bytes that have to move).
+// (26.1 us is 5.5 TB/s of the bytes that have to move).
 constexpr int UPD_THREADS = 128;
 template <typename T, int LP, bool SAME>
-__global__ void __launch_bounds__(UPD_THREADS) sel_update_kernel(SelCall c, bool wide_bc) {
+__global__ void __launch_bounds__(UPD_THREADS, LP > 4 ? 1 : 8) sel_update_kernel(SelCall c, bool wide_bc) {
     constexpr int L = LP ? LP : 1;
     const int i = blockIdx.y, N = c.dstate, lane = threadIdx.x & 31, q = lane % L, per_group = c.channels / c.groups;
     const int d = blockIdx.x * UPD_THREADS + threadIdx.x, d0 = d - q;  // own channel, first of the lane's group
