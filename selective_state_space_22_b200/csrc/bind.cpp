@@ -133,6 +133,11 @@ struct Call {
     }
 };
 void *ptr(const Tensor &t) { return t.defined() && t.numel() ? t.data_ptr() : nullptr; }
+// Whether two contiguous tensors have memory in common.
+bool overlap(const Tensor &a, const Tensor &b) {
+    const char *p = static_cast<const char *>(ptr(a)), *q = static_cast<const char *>(ptr(b));
+    return p && q && p < q + b.nbytes() && q < p + a.nbytes();
+}
 
 int io_of(const Tensor &t, const char *name) {
     if (t.scalar_type() == at::kFloat) return SSD_F32;
@@ -172,12 +177,14 @@ struct Outputs {
         Py_XDECREF(o);
         if (r) throw PythonError();
     }
-    Tensor tensor_of(const Call &c, const char *name, at::ScalarType type, c10::IntArrayRef shape) {
-        PyObject *o = PyDict_GetItemString(d, name);
-        if (!none(o)) return c.given_or_new(o, name, type, shape);
+    Tensor fresh(const Call &c, const char *name, at::ScalarType type, c10::IntArrayRef shape) {
         Tensor t = c.fresh(type, shape);
         set(name, wrap(t));
         return t;
+    }
+    Tensor tensor_of(const Call &c, const char *name, at::ScalarType type, c10::IntArrayRef shape) {
+        PyObject *o = PyDict_GetItemString(d, name);
+        return none(o) ? fresh(c, name, type, shape) : c.given_or_new(o, name, type, shape);
     }
     void absent(const char *name) {
         if (!PyDict_GetItemString(d, name)) {
@@ -455,7 +462,12 @@ PyObject *residual_rmsnorm_bwd(PyObject *const *a) {
     Outputs out(a[7]);
     const Tensor gr = out.tensor_of(c, "dresidual", rtype, shape);
     PyObject *given = PyDict_GetItemString(out.d, "dx");  // a tensor of the caller's is filled in any case
+    if (apart && !none(given) && given == PyDict_GetItemString(out.d, "dresidual")) {
+        out.fresh(c, "dx", type, shape);  // one tensor for both, as a call that does not set them apart leaves it
+        given = PyDict_GetItemString(out.d, "dx");
+    }
     const Tensor gx = apart || !none(given) ? out.tensor_of(c, "dx", type, shape) : Tensor();
+    if (apart && overlap(gx, gr)) throw Refused("out: dx and dresidual share memory, and scale or the residual's dtype sets them apart");
     if (!gx.defined()) out.set("dx", wrap(gr));
     const Tensor gw = out.tensor_of(c, "dweight", at::kFloat, {d}), gs = scaled ? out.tensor_of(c, "dscale", at::kFloat, {d}) : Tensor();
     if (!scaled) out.absent("dscale");

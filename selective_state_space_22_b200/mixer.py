@@ -157,7 +157,8 @@ def ssd_residual_rmsnorm_bwd(residual, weight, dout, dresidual=None, x=None, sca
     """Gradients of ssd_residual_rmsnorm from the r it returned: dict of dresidual (r's
     dtype), dx (dout's dtype; the same tensor where neither scale nor a wider dtype
     sets them apart and ``out`` holds no dx), dweight, and dscale (None without scale,
-    which needs x).  ``out`` may pass them preallocated."""
+    which needs x).  ``out`` may pass them preallocated; where it holds one tensor as both
+    and the call sets them apart, dx becomes a new one."""
     return _run("residual_rmsnorm_bwd", stream, residual, weight, dout, dresidual, x, scale, eps, out)
 
 

@@ -1,0 +1,44 @@
+"""The mixer-block operators where earlier forms of them went wrong: outputs that come back
+in a dict of the caller's, sums that cancel, infinities, growing states, caches without a
+state, streams and errors of other calls."""
+import pytest
+import torch
+
+import mixer_ref as ref
+import selective_state_space_22_b200 as ssd
+from mixer_ref import close, d64
+from test_mixer_gpu import IO, NORM_ROUNDINGS, bounds, gen, randn, sel_inputs, sel_roundings
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    ssd.load_library()
+
+
+# ------------------------------------------------------------- the caller's dict of outputs
+
+def test_scaled_norm_gradient_into_the_dict_of_an_unscaled_call():
+    """Without scale dx and dresidual are one tensor; with scale they differ, and a dict that
+    holds them as one gets a dx of its own."""
+    g, n, d = gen(81), 19, 512
+    r, w, dout, up, x = randn(g, n, d), 1 + randn(g, d, scale=0.1), randn(g, n, d), randn(g, n, d), randn(g, n, d)
+    s = 2 + randn(g, d, scale=0.1)
+    kept = ssd.ssd_residual_rmsnorm_bwd(r, w, dout, up)
+    first = kept["dresidual"]
+    assert kept["dx"] is first
+    want = ssd.ssd_residual_rmsnorm_bwd(r, w, dout, up, x, s)
+    got = ssd.ssd_residual_rmsnorm_bwd(r, w, dout, up, x, s, out=kept)
+    assert got is kept and got["dresidual"] is first and got["dx"] is not first
+    assert all(torch.equal(got[k], want[k]) for k in ("dresidual", "dx", "dweight", "dscale"))
+    # the same memory under two tensors, and memory that overlaps in part, are refused
+    both = torch.empty(n + 1, d, device="cuda")
+    for a, b in ((both[:n], both[:n]), (both[:n], both[1:])):
+        with pytest.raises(ValueError, match="share memory"):
+            ssd.ssd_residual_rmsnorm_bwd(r, w, dout, up, x, s, out=dict(dx=a, dresidual=b))
+    for _ in range(2):  # without scale one tensor for both stays what it was
+        again = ssd.ssd_residual_rmsnorm_bwd(r, w, dout, up, out=dict(dx=first, dresidual=first))
+        assert again["dx"] is first and again["dresidual"] is first and torch.equal(first, want["dresidual"])
