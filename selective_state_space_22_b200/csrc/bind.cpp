@@ -186,11 +186,9 @@ struct Outputs {
         PyObject *o = PyDict_GetItemString(d, name);
         return none(o) ? fresh(c, name, type, shape) : c.given_or_new(o, name, type, shape);
     }
-    void absent(const char *name) {
-        if (!PyDict_GetItemString(d, name)) {
-            Py_INCREF(Py_None);
-            set(name, Py_None);
-        }
+    void absent(const char *name) {  // also over what an earlier call left there
+        Py_INCREF(Py_None);
+        set(name, Py_None);
     }
 };
 

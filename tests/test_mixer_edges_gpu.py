@@ -42,3 +42,27 @@ def test_scaled_norm_gradient_into_the_dict_of_an_unscaled_call():
     for _ in range(2):  # without scale one tensor for both stays what it was
         again = ssd.ssd_residual_rmsnorm_bwd(r, w, dout, up, out=dict(dx=first, dresidual=first))
         assert again["dx"] is first and again["dresidual"] is first and torch.equal(first, want["dresidual"])
+
+
+def test_gradients_of_absent_inputs_are_none_in_a_dict_that_held_them():
+    g, n, d, N = gen(82), 21, 24, 8
+    ins, (D, z, bias) = sel_inputs(g, n, d, 1, N, torch.float32, 0)
+    cu, dy, w, b, nw = bounds([n]), randn(g, n, d), randn(g, d, 4), randn(g, d), 1 + randn(g, d, scale=0.1)
+    _, kept = ssd.ssd_selective_scan_varlen(*ins, cu, D, z, bias, return_chunk_states=True)
+    x = ins[0]
+    calls = [(lambda **o: ssd.ssd_selective_scan_bwd(*ins, cu, dy, kept, D, z, bias, **o),
+              lambda **o: ssd.ssd_selective_scan_bwd(*ins, cu, dy, kept, **o), ("dD", "dz", "ddt_bias")),
+             (lambda **o: ssd.ssd_conv1d_bwd(x, w, b, cu, dy, **o), lambda **o: ssd.ssd_conv1d_bwd(x, w, None, cu, dy, **o), ("dbias",)),
+             (lambda **o: ssd.ssd_residual_rmsnorm_bwd(x, nw, dy, None, x, nw, **o), lambda **o: ssd.ssd_residual_rmsnorm_bwd(x, nw, dy, **o),
+              ("dscale",)),
+             (lambda **o: ssd.ssd_gated_rmsnorm_bwd(x, z, nw, dy, nw, **o), lambda **o: ssd.ssd_gated_rmsnorm_bwd(x, None, nw, dy, **o),
+              ("dz", "dscale"))]
+    for full, bare, absent in calls:
+        out = full()
+        assert all(out[k] is not None for k in absent)
+        want = bare()
+        got = bare(out=out)
+        assert got is out and all(got[k] is None for k in absent), absent
+        assert all(torch.equal(got[k], want[k]) for k in want if want[k] is not None)
+        back = full(out=out)  # and they come again where their inputs do
+        assert all(torch.equal(back[k], v) for k, v in full().items())
