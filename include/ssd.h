@@ -494,8 +494,9 @@ ssd_status ssd_selective_state_update(const ssd_sel_args *args, float *state, co
  * io_dtype (contiguous) and the forward's chunk_states to dx, ddt, dz (NULL when z
  * is) [tokens, channels] and dB, dC [tokens, ngroups, dstate] in io_dtype,
  * contiguous, and dA [channels, dstate], dD and ddt_bias [channels] (or NULL)
- * float32.  Sums run in a fixed order.  The states inside a chunk are formed
- * again.  Two launches (four where sequences are cut) and a workspace.
+ * float32.  Sums run in a fixed order; those over channels (dB, dC) are float32 sums of
+ * products kept to 2^-22.  The states inside a chunk are formed again.  Two launches
+ * (four where sequences are cut) and a workspace.
  */
 size_t ssd_selective_scan_bwd_workspace_size(int tokens, int nseq, int channels, int ngroups, int dstate);
 ssd_status ssd_selective_scan_bwd(const ssd_sel_args *args, const int *cu_seqlens, const void *dy,

@@ -36,12 +36,11 @@ static_assert(SEL_CHUNK == 2 * SUB, "a chunk is two halves");
 // sums of instruction i land in the lanes with lane%4 = i.  Four instructions (the
 // gradients of B and C, four tokens each, of two states) fill D, and three shuffles that
 // halve the values add the groups of a part (the lanes that hold the same states).
-//   float32: each value goes in as two tf32 parts, its first 11 bits and the next 11, so
-//   that it keeps 2^-22; the sums are float32.
-//   bf16: the first part alone.  A value then loses what lies past 11 bits (below
-//   2^-10 of it, a quarter of a step of the bf16 gradient it goes into); the sums are
-//   float32 all the same.
-template <typename T, int SPLIT> struct ChannelSum {
+// Each value goes in as two tf32 parts, its first 11 bits and the next 11, so that it keeps
+// 2^-22; the sums are float32.  bf16 io needs the second part as float32 io does: with the
+// first alone dB and dC shrink by 3.5e-4, and by any amount where channels cancel (forward
+// and gradient of 64 x 512 tokens, 1024 channels, bf16: 1268 us so, 1349 us with both).
+template <int SPLIT> struct ChannelSum {
     static constexpr int GROUPS = 8 / SPLIT;  // of a part
     float d[4];
     __device__ __forceinline__ void clear() { d[0] = d[1] = d[2] = d[3] = 0.f; }
@@ -53,15 +52,11 @@ template <typename T, int SPLIT> struct ChannelSum {
     }
     __device__ __forceinline__ void add(const float (&v)[4], int i, int lane) {
         const float b0 = (lane >> 2) == 2 * i ? 1.f : 0.f, b1 = (lane >> 2) == 2 * i + 1 ? 1.f : 0.f;
-        if constexpr (sizeof(T) == 4) {
-            float x[4], y[4];
+        float x[4], y[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = __uint_as_float(__float_as_uint(v[k]) & 0xffffe000u), y[k] = v[k] - x[k];
-            mma(d, x, b0, b1);
-            mma(d, y, b0, b1);
-        } else {
-            mma(d, v, b0, b1);
-        }
+        for (int k = 0; k < 4; ++k) x[k] = __uint_as_float(__float_as_uint(v[k]) & 0xffffe000u), y[k] = v[k] - x[k];
+        mma(d, x, b0, b1);
+        mma(d, y, b0, b1);
     }
     // Instruction lane%4's sums over the part: out(value, sum) for the values this lane
     // ends with.  d[0..3] are the group's sums of values 0, 2, 1, 3.
@@ -246,7 +241,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
             const float2(*const h_from)[SCAN_THREADS] = half ? sh.hm : sh.h0;
 #pragma unroll 1
             for (int s2 = 0; s2 < NS; s2 += 2) {
-                ChannelSum<T, SPLIT> sums;
+                ChannelSum<SPLIT> sums;
                 sums.clear();
 #pragma unroll
                 for (int s = s2; s < s2 + 2; ++s) {

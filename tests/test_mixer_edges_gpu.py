@@ -66,3 +66,30 @@ def test_gradients_of_absent_inputs_are_none_in_a_dict_that_held_them():
         assert all(torch.equal(got[k], want[k]) for k in want if want[k] is not None)
         back = full(out=out)  # and they come again where their inputs do
         assert all(torch.equal(back[k], v) for k, v in full().items())
+
+
+# ------------------------------------------------------------- sums over channels
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d,G,N", [(64, 1, 4), (60, 2, 8), (35, 1, 16), (128, 2, 32), (200, 1, 64), (66, 3, 7)])
+@pytest.mark.parametrize("lens", [[1] * 13, [37], [5, 0, 8]])
+def test_gradients_of_b_and_c_where_channels_cancel(io, d, G, N, lens):
+    """Products of 13 bits, 241 * 17 = 4097, in one half of a group's channels and -64 * 64 in
+    the other: every partial sum is a whole number below 2^24, so that float32 sums are exact
+    in any order, and the sum is the number of pairs.  (Products cut to 11 bits sum to zero.)
+    The decays are zero, so that each token stands alone; dB takes its products from x and dy
+    as well."""
+    n, io, per = sum(lens), IO[io], d // G
+    half = (torch.arange(d) % per < per // 2).cuda()
+    odd = (torch.arange(d) % per == per - 1).cuda() & (per % 2 == 1)  # without a partner: zero
+    x = torch.where(half, 241.0, 64.0).expand(n, d)
+    dy = torch.where(odd, 0.0, torch.where(half, 17.0, -64.0)).expand(n, d)
+    one = torch.ones(n, G, N, device="cuda", dtype=io)
+    A = torch.full((d, N), -1e30, device="cuda")
+    ins = (x.to(io).contiguous(), torch.ones(n, d, device="cuda", dtype=io), A, one, one)
+    cu = bounds(lens)
+    _, kept = ssd.ssd_selective_scan_varlen(*ins, cu, softplus=False, return_chunk_states=True)
+    got = ssd.ssd_selective_scan_bwd(*ins, cu, dy.to(io).contiguous(), kept, softplus=False)
+    ssd.ssd_get_device_status()
+    for k in ("dB", "dC"):
+        assert (got[k] == per // 2).all(), (k, got[k].flatten()[:4])
