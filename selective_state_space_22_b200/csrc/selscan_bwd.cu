@@ -40,6 +40,8 @@ static_assert(SEL_CHUNK == 2 * SUB, "a chunk is two halves");
 // 2^-22; the sums are float32.  bf16 io needs the second part as float32 io does: with the
 // first alone dB and dC shrink by 3.5e-4, and by any amount where channels cancel (forward
 // and gradient of 64 x 512 tokens, 1024 channels, bf16: 1268 us so, 1349 us with both).
+// The zeros of B turn an infinite (or NaN) value into NaN sums of other tokens and states.
+// `spoilt` sees that in the result, and the half's sums are then taken by shuffles.
 template <int SPLIT> struct ChannelSum {
     static constexpr int GROUPS = 8 / SPLIT;  // of a part
     float d[4];
@@ -57,6 +59,9 @@ template <int SPLIT> struct ChannelSum {
         for (int k = 0; k < 4; ++k) x[k] = __uint_as_float(__float_as_uint(v[k]) & 0xffffe000u), y[k] = v[k] - x[k];
         mma(d, x, b0, b1);
         mma(d, y, b0, b1);
+    }
+    __device__ __forceinline__ float spoilt(float so_far) const {  // NaN from the first sum on that is not finite, else zero
+        return fmaf(d[0], 0.f, fmaf(d[1], 0.f, fmaf(d[2], 0.f, fmaf(d[3], 0.f, so_far))));
     }
     // Instruction lane%4's sums over the part: out(value, sum) for the values this lane
     // ends with.  d[0..3] are the group's sums of values 0, 2, 1, 3.
@@ -83,7 +88,9 @@ template <typename T, int NP> struct BwdShared {
     T x[SEL_CHUNK][CH], dt[SEL_CHUNK][CH], z[SEL_CHUNK][CH], dy[SEL_CHUNK][CH];
     float4 bc[SEL_CHUNK * NP];
     float2 A2[NS][SCAN_THREADS], G[NS][SCAN_THREADS], dA[NS][SCAN_THREADS];
-    float2 h0[NS][SCAN_THREADS], hm[NS][SCAN_THREADS];  // the states before the chunk and before its second half
+    // the states before the chunk and before its second half; once a state of a half has been
+    // read for the last time, hm keeps the G that it met
+    float2 h0[NS][SCAN_THREADS], hm[NS][SCAN_THREADS];
     float part[WARPS][SUB][2][NP];                      // a warp's sums: [token][dB, dC][state]
 };
 
@@ -239,6 +246,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
 #pragma unroll
             for (int k = 0; k < SUB; ++k) du[k] = sd[k] = pre[k] = zero;
             const float2(*const h_from)[SCAN_THREADS] = half ? sh.hm : sh.h0;
+            float spoilt = 0.f;
 #pragma unroll 1
             for (int s2 = 0; s2 < NS; s2 += 2) {
                 ChannelSum<SPLIT> sums;
@@ -260,7 +268,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
                         v[k] = e.x + e.y;
                     }
                     sums.add(v, 2 * (s - s2) + 1, lane);
-                    float2 G = sh.G[s][tid], dA = make_float2(0.f, 0.f);  // of these tokens: one addition to the long sum
+                    const float2 G0 = sh.G[s][tid];  // kept below (a store here cost 6 to 12 % in float32 and at 64 states)
+                    float2 G = G0, dA = make_float2(0.f, 0.f);  // of these tokens: one addition to the long sum
 #pragma unroll
                     for (int k = SUB - 1; k >= 0; --k) {
                         const float4 bc = q[k * NP];
@@ -273,11 +282,58 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
                         const float2 e = mul2(u2[k], g);
                         v[k] = e.x + e.y;
                     }
-                    sh.G[s][tid] = G, sh.dA[s][tid] = add2(sh.dA[s][tid], dA);
+                    sh.G[s][tid] = G, sh.hm[s][tid] = G0, sh.dA[s][tid] = add2(sh.dA[s][tid], dA);
                     sums.add(v, 2 * (s - s2), lane);
                 }
+                spoilt = sums.spoilt(spoilt);
                 const int which = lane & 1, state = state_of(s2 + ((lane >> 1) & 1));  // what instruction lane%4 summed
                 sums.finish(lane, [&](int token, float sum) { sh.part[warp][token][which][state] = sum; });
+            }
+            if (__any_sync(0xffffffffu, spoilt != 0.f)) {
+                // The half again for its sums of dB and dC (and of dA where it holds tokens past
+                // the end, whose states count for nothing; it is the first half taken then).
+                float2 dl0[SUB], u0[SUB], e[OWN];
+#pragma unroll
+                for (int j = 0; j < OWN; ++j) e[j] = own[j];
+                steps_of_half(0);
+#pragma unroll
+                for (int k = 0; k < SUB; ++k) dl0[k] = dl[k], u0[k] = u2[k];
+                steps_of_half(k0);
+#pragma unroll
+                for (int j = 0; j < OWN; ++j) own[j] = e[j];
+#pragma unroll 1
+                for (int s = 0; s < NS; ++s) {
+                    const float2 A2 = sh.A2[s][tid];
+                    float2 h = sh.h0[s][tid], G = sh.hm[s][tid], a[SUB], hp[SUB], dA = zero;
+                    auto put = [&](int token, int which, float2 v2) {
+                        float v = v2.x + v2.y;
+#pragma unroll
+                        for (int o = 1; o < PAIRS; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+                        if (pair == 0) sh.part[warp][token][which][state_of(s)] = v;
+                    };
+                    auto bc = [&](int token) { return sh.bc[token * NP + state_of(s)]; };
+                    if (half)
+#pragma unroll
+                        for (int k = 0; k < SUB; ++k) {
+                            const float2 arg = mul2(dl0[k], A2);
+                            h = fma2(make_float2(ex2a(arg.x), ex2a(arg.y)), h, mul2(u0[k], make_float2(bc(k).x, bc(k).y)));
+                        }
+                    decays(A2, a);
+#pragma unroll
+                    for (int k = 0; k < SUB; ++k) {
+                        hp[k] = h;
+                        h = fma2(a[k], h, mul2(u2[k], make_float2(bc(k0 + k).x, bc(k0 + k).y)));
+                        put(k, 1, mul2(dp[k], h));
+                    }
+#pragma unroll
+                    for (int k = SUB - 1; k >= 0; --k) {
+                        const float2 g = fma2(dp[k], make_float2(bc(k0 + k).z, bc(k0 + k).w), G);
+                        G = mul2(a[k], g);
+                        if (k0 + k < n) dA = fma2(dl[k], mul2(G, hp[k]), dA);
+                        put(k, 0, mul2(u2[k], g));
+                    }
+                    if (k0 + SUB > n) sh.dA[s][tid] = dA;
+                }
             }
             sum_parts<SPLIT>(du, part);
             sum_parts<SPLIT>(sd, part);

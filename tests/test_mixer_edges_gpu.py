@@ -93,3 +93,28 @@ def test_gradients_of_b_and_c_where_channels_cancel(io, d, G, N, lens):
     ssd.ssd_get_device_status()
     for k in ("dB", "dC"):
         assert (got[k] == per // 2).all(), (k, got[k].flatten()[:4])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d,G,N", [(40, 1, 4), (66, 2, 8), (33, 1, 16), (36, 1, 7), (70, 1, 32), (40, 2, 64)])
+@pytest.mark.parametrize("lens,t0", [([5, 30], 17), ([35], 18), ([35], 34), ([6, 2, 27], 7), ([75], 42)])
+def test_an_infinity_reaches_the_gradients_that_have_it_in_their_sums_and_no_other(io, d, G, N, lens, t0):
+    """One infinite x, dy or z of a channel: B's and C's gradients of the other tokens, groups
+    and states, and the other channels' gradients, are what the formulas say.  Decays are mild
+    and every input is away from zero, so that no 0 * infinity arises in the formulas but in
+    what is infinite anyway."""
+    n, io, g, c0 = sum(lens), IO[io], gen(d + t0), d // 2
+    mk = lambda *s: (torch.rand(n, *s, generator=g) + 0.5).to(io).cuda()  # noqa: E731
+    cu, A = bounds(lens), -(torch.rand(d, N, generator=g) * 2 + 0.1).cuda()
+    for where in ("x", "dy"):
+        x, dt, B, C, dy = mk(d), mk(d) * 0.1, mk(G, N), mk(G, N), mk(d)
+        (x if where == "x" else dy)[t0, c0] = float("inf")
+        want = ref.sel_bwd(d64(x), d64(dt), d64(A), d64(B), d64(C), cu, d64(dy), softplus=False)
+        _, kept = ssd.ssd_selective_scan_varlen(x, dt, A, B, C, cu, softplus=False, return_chunk_states=True)
+        got = ssd.ssd_selective_scan_bwd(x, dt, A, B, C, cu, dy, kept, softplus=False)
+        ssd.ssd_get_device_status()
+        r = 2 * sel_roundings(max(lens), N, (x, dt, A), (None,) * 3, False) + d
+        for k in ("dx", "ddt", "dA", "dB", "dC"):
+            v, m = want[k]
+            assert torch.equal(torch.isfinite(d64(got[k])), torch.isfinite(v)), (where, k)
+            close(got[k], v, m, r + n, k, torch.isfinite(v))
