@@ -457,7 +457,7 @@ ssd_status ssd_conv1d_bwd(const void *xbc, long long xbc_stride, const float *we
  *  A [channels, dstate], D and dt_bias [channels] (or NULL) float32
  *  dstate    1 .. 64.
  *  delta A <= 0 is expected, as for the other scans (a state that grows is computed
- *  as long as its growth over 512 tokens fits a float32).
+ *  as long as it, and its growth over one token, fit a float32).
  */
 typedef struct {
     const void *x, *dt, *z, *B, *C;

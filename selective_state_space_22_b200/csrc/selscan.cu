@@ -186,6 +186,17 @@ __global__ void __launch_bounds__(SCAN_THREADS, FWD_BLOCKS_PER_SM) sel_fwd_kerne
     }
 }
 
+// 2^x h + S for a whole segment's x.  The factor alone may leave float32 where the product
+// does not (a state that grew, or grows): it is taken in three parts then.  From the
+// largest float32 to the smallest it is 2^277, so that a part that overflows or vanishes
+// belongs to a result that does; and nothing stays nothing.
+__device__ __forceinline__ float carry(float x, float h, float S) {
+    if (fabsf(x) <= 126.f) return fmaf(ex2a(x), h, S);
+    if (h == 0.f) return S;
+    const float part = ex2a(x * (1.f / 3.f));
+    return fmaf(part, part * (part * h), S);
+}
+
 // A thread per (sequence, state, channel) goes through the sequence's segments.
 __global__ void __launch_bounds__(128) sel_join_kernel(SelCall c, Segments sg, bool backwards) {
     const int i = blockIdx.x, n = blockIdx.z, d = blockIdx.y * 128 + threadIdx.x, N = c.dstate;
@@ -213,7 +224,7 @@ __global__ void __launch_bounds__(128) sel_join_kernel(SelCall c, Segments sg, b
         for (int u = 0; u < BATCH; ++u) {
             const int j = j0 + u, k = backwards ? count - 1 - j : j;
             if (j < count) at[k * step] = h;
-            h = fmaf(ex2a(A2 * w[u]), h, S[u]);
+            h = carry(A2 * w[u], h, S[u]);
         }
     }
 }

@@ -118,3 +118,50 @@ def test_an_infinity_reaches_the_gradients_that_have_it_in_their_sums_and_no_oth
             v, m = want[k]
             assert torch.equal(torch.isfinite(d64(got[k])), torch.isfinite(v)), (where, k)
             close(got[k], v, m, r + n, k, torch.isfinite(v))
+
+
+# ------------------------------------------------------------- states that grow
+
+def grow_case(lens, d, N, g):
+    """Steps below zero for 40 tokens of each sequence (states grow by 2^200 in all there)
+    from states of about 2^-107, then steps above zero that take it back; before that, states
+    of zero through a growth of 2^200.  No input lies near zero, so that what grows has its
+    24 bits."""
+    n = sum(lens)
+    away = lambda *s: (torch.rand(s, generator=g) + 0.5) * (torch.randint(2, s, generator=g) * 2 - 1)  # noqa: E731
+    A = -torch.linspace(0.9, 1.0, d * N).reshape(d, N)
+    dt, x = torch.full((n, d), 0.01), torch.zeros(n, d)
+    at = 0
+    for length in lens:
+        dt[at + 8:at + 48] = -200 / 1.4427 / 40        # from nothing: stays nothing
+        x[at + 60] = away(d) * 2.0 ** -100
+        dt[at + 80:at + 120] = -200 / 1.4427 / 40      # up to about 2^93
+        dt[at + 128:at + 168] = 200 / 1.4427 / 40      # and back
+        x[at + 170:at + length] = away(length - 170, d)
+        at += length
+    B, C = away(n, 1, N), away(n, 1, N)
+    return [t.cuda() for t in (x, dt, A.contiguous(), B, C)]
+
+
+@pytest.mark.parametrize("lens,d,N", [([300], 6, 4), ([200, 250], 40, 16), ([2600], 4096, 2)])
+def test_states_that_grow_within_float32(lens, d, N):
+    """No product of decays but a state itself has to fit a float32, wherever the sequence is cut."""
+    g = gen(83)
+    ins, cu = grow_case(lens, d, N, g), bounds(lens)
+    state = torch.zeros(len(lens), d, N, device="cuda")
+    y, kept = ssd.ssd_selective_scan_varlen(*ins, cu, softplus=False, state=state, return_chunk_states=True)
+    want, mag, end, mend, _ = ref.sel(*map(d64, ins), cu, softplus=False)
+    # exponents of 139 twice on the way: as rounded products over 40 tokens (3 * 139 roundings
+    # of the argument and 6 per token), or as a sum of a segment's steps, here of 96 tokens at
+    # most, each addition rounded
+    r = 2 * (3 * 139 + 6 * 40 + 96 * 139)
+    close(y, want, mag, r, "y")
+    close(state, end, mend, r, "state")
+    dy = torch.zeros_like(y)
+    for lo, hi in ref.spans(cu):
+        dy[lo + 62] = randn(g, d, scale=2.0 ** -100)  # backwards: the later growth meets no gradient, the earlier a small one
+    got = ssd.ssd_selective_scan_bwd(*ins, cu, dy, kept, softplus=False)
+    grads = ref.sel_bwd(*map(d64, ins), cu, d64(dy), softplus=False)
+    ssd.ssd_get_device_status()
+    for k in ("dx", "ddt", "dA", "dB", "dC"):
+        close(got[k], *grads[k], 2 * r + d + (sum(lens) if k == "dA" else 0), k)
