@@ -237,9 +237,15 @@ __global__ void __launch_bounds__(128) sel_join_kernel(SelCall c, Segments sg, b
 // their channels together measured 43.6 us against 27.5 us for 256 x 4096 channels
 // of 16 states: five times the instructions; 64 registers, so that eight blocks are on an
 // SM, 26.1 us, 48 31.7 us.)  LP = 0: any dstate, a lane per channel.
+// As in the scan, a step of nothing is a decay of one, also where A is -infinity: A is kept
+// from -1e38 on, where a step above 1e-36 leaves nothing.
 // SAME: the warp's channels lie in one B/C group.  Bound by HBM: the state in and out
 // (26.1 us is 5.5 TB/s of the bytes that have to move).
 constexpr int UPD_THREADS = 128;
+__device__ __forceinline__ float finite_rate(float A) { return A < -1e38f ? -1e38f : A; }
+__device__ __forceinline__ float4 finite_rates(float4 a) {
+    return make_float4(finite_rate(a.x), finite_rate(a.y), finite_rate(a.z), finite_rate(a.w));
+}
 template <typename T, int LP, bool SAME>
 __global__ void __launch_bounds__(UPD_THREADS, LP > 4 ? 1 : 8) sel_update_kernel(SelCall c, bool wide_bc) {
     constexpr int L = LP ? LP : 1;
@@ -255,7 +261,7 @@ __global__ void __launch_bounds__(UPD_THREADS, LP > 4 ? 1 : 8) sel_update_kernel
     float4 a[L];
     if constexpr (LP > 0 && LP <= 4)  // registers allow it
 #pragma unroll
-        for (int u = 0; u < L; ++u) a[u] = __ldg(reinterpret_cast<const float4 *>(c.A + (size_t)min(d0 + u, last) * N) + q);
+        for (int u = 0; u < L; ++u) a[u] = finite_rates(__ldg(reinterpret_cast<const float4 *>(c.A + (size_t)min(d0 + u, last) * N) + q));
     const int slot = slot_of(c.seq.slots, c.seq.nslots, i, c.seq.dev_error);
     if (slot < 0) return;
     float *st = c.state + (size_t)slot * c.channels * N;
@@ -279,7 +285,7 @@ __global__ void __launch_bounds__(UPD_THREADS, LP > 4 ? 1 : 8) sel_update_kernel
         for (int u = 0; u < L; ++u) {
             const int du_ = min(d0 + u, last);
             if (!SAME) load_bc(du_ / per_group);
-            if (LP > 4) a[u] = __ldg(reinterpret_cast<const float4 *>(c.A + (size_t)du_ * N) + q);
+            if (LP > 4) a[u] = finite_rates(__ldg(reinterpret_cast<const float4 *>(c.A + (size_t)du_ * N) + q));
             const float s2 = __shfl_sync(0xffffffffu, d2, u, L), su = __shfl_sync(0xffffffffu, du, u, L);
             h[u].x = fmaf(ex2a(s2 * a[u].x), h[u].x, su * b[0]);
             h[u].y = fmaf(ex2a(s2 * a[u].y), h[u].y, su * b[1]);
@@ -303,7 +309,7 @@ __global__ void __launch_bounds__(UPD_THREADS, LP > 4 ? 1 : 8) sel_update_kernel
         const int g = d / per_group;
         for (int n = 0; n < N; ++n) {
             float *hn = st + (size_t)d * N + n;
-            *hn = fmaf(ex2a(d2 * c.A[(size_t)d * N + n]), *hn, du * ld_f32<T>(B + g * N + n));
+            *hn = fmaf(ex2a(d2 * finite_rate(c.A[(size_t)d * N + n])), *hn, du * ld_f32<T>(B + g * N + n));
             y = fmaf(ld_f32<T>(C + g * N + n), *hn, y);
         }
     }

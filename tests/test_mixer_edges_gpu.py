@@ -165,3 +165,30 @@ def test_states_that_grow_within_float32(lens, d, N):
     ssd.ssd_get_device_status()
     for k in ("dx", "ddt", "dA", "dB", "dC"):
         close(got[k], *grads[k], 2 * r + d + (sum(lens) if k == "dA" else 0), k)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d,N", [(40, 4), (33, 16), (40, 64), (9, 7), (96, 32)])
+def test_a_token_with_a_step_of_nothing_is_the_scans(io, d, N):
+    """A = -infinity and a step of exactly zero: the token leaves the state as it was, as it
+    does inside a prompt (and any other step forgets it)."""
+    g, b = gen(84), 3
+    x, B, C = (randn(g, b, *s, io=IO[io]) for s in ((d,), (1, N), (1, N)))
+    dt = torch.zeros(b, d, device="cuda", dtype=IO[io])
+    dt[1] = 0.5
+    A = -randn(g, d, N).abs()
+    A[:, 0], A[1, N - 1] = -float("inf"), -3e38
+    start = randn(g, b, d, N)
+    one, whole = start.clone(), start.clone()
+    y = ssd.ssd_selective_state_update(one, x, dt, A, B, C, softplus=False)
+    has = torch.ones(b, dtype=torch.bool, device="cuda")
+    yw, _ = ssd.ssd_selective_scan_varlen(x, dt, A, B, C, bounds([1] * b), softplus=False, state=whole, has_init=has)
+    ssd.ssd_get_device_status()
+    assert torch.isfinite(one).all() and torch.isfinite(y).all()
+    for i in (0, 2):
+        assert torch.equal(one[i], start[i]) and torch.equal(whole[i], start[i])
+    fresh = (dt[1].double() * x[1].double())[:, None] * B[1, 0].double()
+    assert ((one[1, :, 0].double() - fresh[:, 0]).abs() <= 2 * 2.0 ** -24 * fresh[:, 0].abs()).all()
+    # per state and token: exponential (argument rounded, 2^-22 of its own), three products
+    tol = 40 * 2.0 ** -24 * (start.abs() + fresh.float().abs() + 1)
+    assert ((one - whole).abs() <= tol).all()
