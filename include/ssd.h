@@ -422,7 +422,8 @@ ssd_status ssd_conv1d_varlen(const void *xbc, long long xbc_stride, const float 
                              void *stream);
 
 /* One token per sequence: xbc [batch, channels]; conv_state is read and moved on
- * in place.  batch <= 65535. */
+ * in place (width 1 has none: NULL, and slots only says which rows to skip).
+ * batch <= 65535. */
 ssd_status ssd_conv1d_update(void *conv_state, const int *slots, const void *xbc,
                              long long xbc_stride, const float *weight, const float *bias,
                              void *x_out, void *B_out, void *C_out, ssd_dtype io_dtype, int batch,

@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(128) conv_update_kernel(const T *__restrict__ 
                                                          T *__restrict__ state, int cx, int cb, int K, int silu,
                                                          Packed p) {
     const int ctot = cx + 2 * cb, c = blockIdx.x * 128 + threadIdx.x, i = blockIdx.y;
-    const int slot = slot_of(p.slots, p.nslots, i, p.dev_error);
+    // one tap has no state to find: only a padding entry is skipped then
+    const int slot = K > 1 ? slot_of(p.slots, p.nslots, i, p.dev_error) : p.slots ? min(p.slots[i], 0) : 0;
     if (slot < 0 || c >= ctot) return;
     T *st = state + ((size_t)slot * ctot + c) * (K - 1);
     const T xv = in[i * ld + c];

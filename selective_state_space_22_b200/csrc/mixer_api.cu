@@ -173,6 +173,7 @@ ssd_status ssd_conv1d_update(void *conv_state, const int *slots, const void *xbc
     if (s == SSD_OK) s = check_slots(conv_state, slots, nslots, batch);
     if (s != SSD_OK || batch == 0) return s;
     if (width > 1) NEED(conv_state);
+    if (!on(slots, 4)) return refuse(SSD_ERR_INVALID_ARG, "slots is not aligned to its elements");
     NEED(xbc);
     NEED(weight);
     NEED(x_out);

@@ -1,6 +1,8 @@
 """The mixer-block operators where earlier forms of them went wrong: outputs that come back
 in a dict of the caller's, sums that cancel, infinities, growing states, caches without a
 state, streams and errors of other calls."""
+import ctypes
+
 import pytest
 import torch
 
@@ -192,3 +194,31 @@ def test_a_token_with_a_step_of_nothing_is_the_scans(io, d, N):
     # per state and token: exponential (argument rounded, 2^-22 of its own), three products
     tol = 40 * 2.0 ** -24 * (start.abs() + fresh.float().abs() + 1)
     assert ((one - whole).abs() <= tol).all()
+
+
+# ------------------------------------------------------------- caches without a state
+
+def test_conv_of_one_tap_has_no_state_to_find():
+    """Width 1: the C call takes no cache, the Python call one of no elements, of any number of
+    slots; a negative slot still skips its row."""
+    g, b, d = gen(85), 5, 12
+    x, w, cb = randn(g, b, d), randn(g, d, 1), randn(g, d)
+    want, mag, _ = ref.conv(d64(x), d64(w), d64(cb), torch.arange(b + 1), True)
+    out = torch.full((b, d), 7.0, device="cuda")
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    lib = ssd.load_library()
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert lib.ssd_conv1d_update(None, None, p(x), d, p(w), p(cb), p(out), None, None, 0, b, 0, d, 0, 1, 1, stream) == ssd.SSD_OK
+    ssd.ssd_get_device_status()
+    close(out, want, mag, 40)
+    for nslots in (0, 2, b):
+        got = ssd.ssd_conv1d_update(torch.empty(nslots, d, 0, device="cuda"), x, w, cb)[0]
+        ssd.ssd_get_device_status()
+        close(got, want, mag, 40)
+    out.fill_(7)
+    slots = torch.tensor([4, -1, 0, 9, 4], dtype=torch.int32).cuda()
+    ssd.ssd_conv1d_update(torch.empty(0, d, 0, device="cuda"), x, w, cb, slots=slots, out=(out, out[:, :0].contiguous(), out[:, :0].contiguous()))
+    ssd.ssd_get_device_status()
+    live = slots.cpu() >= 0
+    close(out[live.cuda()], want[live], mag[live], 40)
+    assert (out[1] == 7).all()
