@@ -152,6 +152,11 @@ size_t sized(size_t n, const char *what) {
     return n;
 }
 
+// A cache of no slots is a cache, in which no sequence has a state: it goes in as this
+// address, which nothing follows (a slot below zero is none, any other out of range).
+alignas(16) char no_slots[16];
+void *cache(void *p, int nslots) { return nslots ? p : no_slots; }
+
 PyObject *status(int s) { return PyLong_FromLong(s); }
 PyObject *wrap(Tensor t) { return THPVariable_Wrap(std::move(t)); }
 
@@ -225,6 +230,10 @@ struct ConvIn {
         w = static_cast<const float *>(c.whole(weight, "weight", at::kFloat, {ct, width}));
         b = static_cast<const float *>(c.maybe(a[2], "bias", at::kFloat, {ct}));
     }
+    void *state(const Tensor &t, int nslots) const {  // one tap has none
+        void *p = c.whole(t, "conv_state", xbc.scalar_type(), {nslots, ct, width - 1});
+        return width > 1 ? cache(p, nslots) : nullptr;
+    }
     void outputs(PyObject *given, Tensor (&t)[3]) const {
         const int widths[3] = {cx, cb, cb};
         const char *const names[3] = {"x", "B", "C"};
@@ -263,7 +272,7 @@ PyObject *conv1d_varlen(PyObject *const *a) {
     if (!none(a[7])) {
         need_dim(tensor(a[7], "conv_state"), "conv_state", 3);
         nslots = size32(tensor(a[7], "conv_state").size(0), "conv_state");
-        state = in.c.whole(a[7], "conv_state", in.xbc.scalar_type(), {nslots, in.ct, in.width - 1});
+        state = in.state(tensor(a[7], "conv_state"), nslots);
     }
     const int *slots = static_cast<const int *>(in.c.maybe(a[8], "slots", at::kInt, {seq.n}));
     const auto *has = static_cast<const unsigned char *>(in.c.maybe(a[9], "has_init", at::kBool, {seq.n}));
@@ -280,7 +289,7 @@ PyObject *conv1d_update(PyObject *const *a) {
     const Tensor &st = tensor(a[3], "conv_state");
     need_dim(st, "conv_state", 3);
     const int nslots = size32(st.size(0), "conv_state");
-    void *state = in.c.whole(st, "conv_state", in.xbc.scalar_type(), {nslots, in.ct, in.width - 1});
+    void *state = in.state(st, nslots);
     const int *slots = static_cast<const int *>(in.c.maybe(a[7], "slots", at::kInt, {in.n}));
     Tensor t[3];
     in.outputs(a[8], t);
@@ -352,7 +361,7 @@ struct SelIn {
         const Tensor &t = tensor(o, "state");
         need_dim(t, "state", 3);
         nslots = size32(t.size(0), "state");
-        return static_cast<float *>(c.whole(t, "state", at::kFloat, {nslots, d, N}));
+        return static_cast<float *>(cache(c.whole(t, "state", at::kFloat, {nslots, d, N}), nslots));
     }
 };
 

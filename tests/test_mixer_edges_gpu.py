@@ -212,7 +212,9 @@ def test_conv_of_one_tap_has_no_state_to_find():
     ssd.ssd_get_device_status()
     close(out, want, mag, 40)
     for nslots in (0, 2, b):
-        got = ssd.ssd_conv1d_update(torch.empty(nslots, d, 0, device="cuda"), x, w, cb)[0]
+        cache = torch.empty(nslots, d, 0, device="cuda")
+        close(ssd.ssd_conv1d_varlen(x, w, cb, bounds([2, 3]), conv_state=cache)[0], want, mag, 40)
+        got = ssd.ssd_conv1d_update(cache, x, w, cb)[0]
         ssd.ssd_get_device_status()
         close(got, want, mag, 40)
     out.fill_(7)
@@ -222,3 +224,29 @@ def test_conv_of_one_tap_has_no_state_to_find():
     live = slots.cpu() >= 0
     close(out[live.cuda()], want[live], mag[live], 40)
     assert (out[1] == 7).all()
+
+
+def test_a_cache_of_no_slots_is_no_missing_cache():
+    """Sequences have no state to find in a cache of no slots: refused where the sequence's
+    number is its slot, reported where `slots` names one; padding entries are skipped."""
+    g, n, d, N = gen(86), 10, 16, 4
+    (x, dt, A, B, C), _ = sel_inputs(g, n, d, 1, N, torch.float32, 0)
+    cu, w = bounds([4, 6]), randn(g, d, 4)
+    state, conv_state = torch.empty(0, d, N, device="cuda"), torch.empty(0, d, 3, device="cuda")
+    calls = [lambda s: ssd.ssd_selective_scan_varlen(x, dt, A, B, C, cu, state=state, slots=s)[0],
+             lambda s: ssd.ssd_selective_state_update(state, x[:2], dt[:2], A, B[:2], C[:2], slots=s),
+             lambda s: ssd.ssd_conv1d_varlen(x, w, None, cu, conv_state=conv_state, slots=s)[0],
+             lambda s: ssd.ssd_conv1d_update(conv_state, x[:2], w, slots=s)[0]]
+    for call in calls:
+        with pytest.raises(ssd.SSDError, match="0 states for 2 sequences"):
+            call(None)
+        call(torch.tensor([0, -1], dtype=torch.int32).cuda())
+        with pytest.raises(ssd.SSDError) as e:
+            ssd.ssd_get_device_status()
+        assert e.value.status == ssd.SSD_ERR_INVALID_ARG
+        call(torch.tensor([-1, -1], dtype=torch.int32).cuda())
+        ssd.ssd_get_device_status()
+    none = torch.tensor([-1, -1], dtype=torch.int32).cuda()
+    assert torch.equal(calls[0](none), ssd.ssd_selective_scan_varlen(x, dt, A, B, C, cu)[0])
+    assert torch.equal(calls[2](none), ssd.ssd_conv1d_varlen(x, w, None, cu)[0])
+    ssd.ssd_get_device_status()
