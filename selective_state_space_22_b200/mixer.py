@@ -69,6 +69,9 @@ def _load():
 
 def _run(name, stream, *args):
     if stream is not None:
+        device = getattr(args[0], "device", stream.device)  # the first argument's is the call's
+        if device.type == "cuda" and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
         with torch.cuda.stream(stream):
             return _run(name, None, *args)
     r = getattr(_native or _load(), name)(*args)
