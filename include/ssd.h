@@ -568,7 +568,8 @@ ssd_status ssd_gated_rmsnorm_bwd(const void *y, long long y_stride, const void *
  * tensor-core kernel's bounded waits between its warp roles gave up after 1 s;
  * the kernel then stops at once and the outputs of that call are invalid), or a
  * CUDA error from the stream; SSD_ERR_INVALID_ARG when sequence bounds or slots
- * in device memory were out of range (see the packed sequences above).
+ * in device memory were out of range (see the packed sequences above; where a wait
+ * gave up too, the next call reports it).
  * SSD_OK when there was none.
  */
 ssd_status ssd_get_device_status(void *stream);

@@ -267,8 +267,8 @@ size_t norm_bwd_workspace(int rows, int width);
 cudaError_t launch_norm_before_bwd(const NormCall &c, float *ws, cudaStream_t st);
 cudaError_t launch_norm_after_bwd(const NormCall &c, float *ws, cudaStream_t st);
 
-// The device error word of the current device (set by kernels, read by
-// ssd_get_device_status); NULL with ssd_last_error set when it cannot be had.
+// The current device's error word of bounds and slots (set by kernels, read by
+// ssd_get_device_status; a wait that gave up has a word of its own); NULL with ssd_last_error set when it cannot be had.
 int *device_error_word();
 
 }  // namespace ssd

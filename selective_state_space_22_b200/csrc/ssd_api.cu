@@ -15,9 +15,10 @@
 #include "mixer.cuh"
 #include "ssd_internal.cuh"
 
-// First device-side error raised by a kernel of this library on this device
-// (a bounded wait that gave up).  Read and cleared by ssd_get_device_status.
-__device__ int g_ssd_device_error = 0;
+// First device-side errors raised by kernels of this library on this device: a bounded
+// wait that gave up, and bounds or slots out of range (neither hides the other).  Read and
+// cleared by ssd_get_device_status.
+__device__ int g_ssd_device_error[2] = {0, 0};
 
 namespace {
 
@@ -290,7 +291,8 @@ void set_last_error(const char *msg) { g_last_error = msg; }
 
 int *device_error_word() {
     ssd_status st = SSD_OK;
-    return device_error_ptr(&st);
+    int *p = device_error_ptr(&st);
+    return p ? p + 1 : nullptr;
 }
 
 void *current_context() {
@@ -543,12 +545,12 @@ ssd_status ssd_get_device_status(void *stream) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-    int code = 0;
-    e = cudaMemcpyFromSymbol(&code, g_ssd_device_error, sizeof(int));
-    if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
+    int codes[2] = {0, 0};
+    e = cudaMemcpyFromSymbol(codes, g_ssd_device_error, sizeof(codes));
+    if (e != cudaSuccess) return cuda_fail(e, "reading the device error words");
+    const int at = codes[0] ? 0 : 1, code = codes[at], zero = 0;
     if (code == 0) return SSD_OK;
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_ssd_device_error, &zero, sizeof(int));
+    e = cudaMemcpyToSymbol(g_ssd_device_error, &zero, sizeof(int), at * sizeof(int));
     if (e != cudaSuccess) return cuda_fail(e, "clearing the device error word");
     if (code == ssd::DEV_TIMEOUT)
         return fail(SSD_ERR_TIMEOUT, "a bounded inter-block wait gave up on the device; the "

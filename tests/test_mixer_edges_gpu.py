@@ -9,6 +9,8 @@ import torch
 import mixer_ref as ref
 import selective_state_space_22_b200 as ssd
 from mixer_ref import close, d64
+from parity import to_dev
+from selective_state_space_22_b200 import inputs
 from test_mixer_gpu import IO, NORM_ROUNDINGS, bounds, gen, randn, sel_inputs, sel_roundings
 
 pytestmark = pytest.mark.gpu
@@ -250,3 +252,33 @@ def test_a_cache_of_no_slots_is_no_missing_cache():
     assert torch.equal(calls[0](none), ssd.ssd_selective_scan_varlen(x, dt, A, B, C, cu)[0])
     assert torch.equal(calls[2](none), ssd.ssd_conv1d_varlen(x, w, None, cu)[0])
     ssd.ssd_get_device_status()
+
+
+# ------------------------------------------------------------- errors of other calls
+
+def test_bad_bounds_do_not_hide_a_timeout():
+    """A wait that gave up invalidates a whole call, so it is reported first, whatever bounds
+    or slots were refused before it; the refusal is reported by the next status call."""
+    shape = inputs.ScanShape("stall", 2, 2048, 8, 64, 1, 128, 128, "bf16", init_state=True, seed=31)
+    scan = to_dev(inputs.scan_inputs(shape))
+    g = gen(87)
+    x, w = randn(g, 10, 16), randn(g, 16, 4)
+    bad = torch.tensor([0, 99], dtype=torch.int32).cuda()
+    lib = ssd.load_library()
+    ssd.ssd_get_device_status()
+    for first in (True, False):
+        try:
+            if first:
+                ssd.ssd_conv1d_varlen(x, w, None, bad)
+            assert lib.ssd_debug_inject_stall(1, 10_000_000) == ssd.SSD_OK
+            ssd.ssd_scan_fwd(scan["x"], scan["dt"], scan["A"], scan["B"], scan["C"], scan["D"], scan["init_state"], chunk_size=128)
+            torch.cuda.synchronize()
+        finally:
+            lib.ssd_debug_inject_stall(0, 0)
+        if not first:
+            ssd.ssd_conv1d_varlen(x, w, None, bad)
+        for status in (ssd.SSD_ERR_TIMEOUT, ssd.SSD_ERR_INVALID_ARG):
+            with pytest.raises(ssd.SSDError) as e:
+                ssd.ssd_get_device_status()
+            assert e.value.status == status
+        ssd.ssd_get_device_status()
