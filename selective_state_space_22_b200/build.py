@@ -17,6 +17,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +26,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libssd.so")
 BIND = os.path.join(PKG, "_bind.so")
+BIND_FOR = os.path.join(BUILD, "_bind.for")  # the Python and torch that BIND was built against
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
@@ -51,6 +53,23 @@ def _stale(out: str, deps) -> bool:
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _bind_for() -> str:
+    from importlib.metadata import version
+
+    return f"{sys.version}\ntorch {version('torch')}\n"
+
+
+def _bind_stale() -> bool:
+    """Whether the binding is older than its sources or was built against another Python or torch."""
+    if _stale(BIND, [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "ssd.h"), __file__]):
+        return True
+    try:
+        with open(BIND_FOR) as f:
+            return f.read() != _bind_for()
+    except OSError:
+        return True
 
 
 def _bind_command() -> list[str]:
@@ -85,7 +104,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)
     bind_tmp = None
-    if force or _stale(BIND, [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "ssd.h"), __file__]):
+    if force or _bind_stale():
         bind_tmp = BIND + f".tmp{os.getpid()}"
         jobs.append([*_bind_command(), "-o", bind_tmp])
 
@@ -101,6 +120,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 print(out)
     if bind_tmp:
         os.replace(bind_tmp, BIND)
+        with open(BIND_FOR, "w") as f:
+            f.write(_bind_for())
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])

@@ -34,3 +34,14 @@ def test_a_stream_of_another_device_is_refused():
                  lambda: ssd.ssd_gated_rmsnorm_bwd(x, w, w, w, stream=at(1))):
         with pytest.raises(ValueError, match="stream is on cuda:1, the tensors are on cuda:0"):
             call()
+
+
+def test_the_binding_is_built_again_for_another_torch(lib, monkeypatch):
+    assert not ssd_build._bind_stale()
+    mine = ssd_build._bind_for()
+    assert torch.__version__.split("+")[0] in mine
+    monkeypatch.setattr(ssd_build, "_bind_for", lambda: mine.replace("torch ", "torch 9"))
+    assert ssd_build._bind_stale()
+    monkeypatch.undo()
+    monkeypatch.setattr(ssd_build, "BIND_FOR", ssd_build.BIND_FOR + ".missing")
+    assert ssd_build._bind_stale()
