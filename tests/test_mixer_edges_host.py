@@ -4,7 +4,9 @@ import types
 import pytest
 import torch
 
+import mixer_ref as ref
 import selective_state_space_22_b200 as ssd
+from mixer_bounds import Scan
 from selective_state_space_22_b200 import build as ssd_build
 
 FAKE = 1 << 20  # 16-byte aligned, never dereferenced
@@ -45,3 +47,28 @@ def test_the_binding_is_built_again_for_another_torch(lib, monkeypatch):
     monkeypatch.undo()
     monkeypatch.setattr(ssd_build, "BIND_FOR", ssd_build.BIND_FOR + ".missing")
     assert ssd_build._bind_stale()
+
+
+@pytest.mark.parametrize("softplus", [True, False])
+def test_the_bounded_formulas_are_the_formulas(softplus):
+    """mixer_bounds.Scan has mixer_ref's values, and its bounds hold a float32 evaluation
+    without being longer than a few hundred roundings of what is summed."""
+    g, n, d, G, N = torch.Generator().manual_seed(3), 60, 12, 2, 5
+    r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    x, dt, A, B, C, dy = r(n, d), r(n, d), -torch.rand(d, N, generator=g) * 15 - 1, r(n, G, N), r(n, G, N), r(n, d)
+    cu, opt = torch.tensor([0, 25, 25, 26, 60]), (r(d), r(n, d), r(d) * 0.5 - 2.5) if softplus else (None, None, None)
+    dt = dt if softplus else dt.abs() * 0.1
+    d64 = ref.d64
+    ins, opt64 = [d64(t) for t in (x, dt, A, B, C)], [d64(t) for t in opt]
+    scan = Scan(*ins, cu, *opt64, softplus=softplus)
+    y, mag, end, mend, _ = ref.sel(*ins, cu, *opt64, softplus=softplus)
+    assert torch.allclose(scan.y, y, rtol=1e-12) and torch.allclose(scan.end, end, rtol=1e-12)
+    assert (scan.ey <= 500 * mag).all() and (scan.eend <= 500 * mend).all()
+    want = ref.sel_bwd(*ins, cu, d64(dy), *opt64, softplus=softplus)
+    for k, (v, e) in scan.bwd(d64(dy)).items():
+        assert torch.allclose(v, want[k][0], rtol=1e-11, atol=1e-13), k
+        assert (e <= 2000 * want[k][1] + 1e-30).all(), k
+    h, delta = torch.zeros(d, N), torch.nn.functional.softplus(dt + opt[2]) if softplus else dt  # in float32
+    for t in range(25):
+        h = torch.exp(delta[t][:, None] * A) * h + (delta[t] * x[t])[:, None] * B[t].repeat_interleave(d // G, 0)
+    assert ((h.double() - scan.end[0]).abs() <= ref.U32 * scan.eend[0]).all()
