@@ -187,20 +187,12 @@ __global__ void __launch_bounds__(SCAN_THREADS, FWD_BLOCKS_PER_SM) sel_fwd_kerne
 }
 
 // 2^x h + S for a whole segment's x.  The factor alone may leave float32 where the product
-// does not (a state that grew, or grows), so it goes in as three that do not: from the
-// largest float32 to the smallest it is 2^277.  For |x| <= 126 the first is all of it and
-// the others are one.  Without branches, since the segments of a sequence are a serial chain
-// and states with large |A| are always past 126: asking cost sel_join 12.3 and 14.5 us at
-// twelve prompts and at one of 16384 tokens, 11.7 and 13.0 us so.
+// does not (a state that grew, or grows), so it goes in as two that do not: past 2^254 every
+// normal float32 overflows, and past 2^-252 the second factor is zero.  From -126 to 127 the
+// first is all of it.
 __device__ __forceinline__ float carry(float x, float h, float S) {
-    float f[3];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        const float part = fminf(fmaxf(x, -126.f), 126.f);
-        f[k] = ex2a(part);
-        x -= part;
-    }
-    return fmaf(f[0], f[1] * (f[2] * h), S);
+    const float part = fminf(fmaxf(x, -126.f), 127.f);
+    return fmaf(ex2a(part), ex2a(fminf(x - part, 127.f)) * h, S);
 }
 
 // A thread per (sequence, state, channel) goes through the sequence's segments.
