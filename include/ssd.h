@@ -402,8 +402,8 @@ ssd_status ssd_scan_bwd_complex(const float *x, const float *dt, const float *A,
  * projection's output go in as they are; such inputs need their element's
  * alignment only (16-byte aligned rows are read wider).  Inner strides are 1.
  * All other tensors are contiguous and 16-byte aligned.  Arithmetic is float32
- * whatever io_dtype, rounded once on output.  Nothing is allocated; a workspace
- * needs no initialisation and serves one call at a time.
+ * whatever io_dtype (exponentials to 2^-22), rounded once on output.  Nothing is
+ * allocated; a workspace needs no initialisation and serves one call at a time.
  */
 
 /*
@@ -475,7 +475,9 @@ typedef struct {
  *  state  [nslots, channels, dstate] float32, or NULL: every sequence from zero
  *  chunk_states  NULL, or [ssd_selective_scan_chunk_states(tokens, nseq), dstate,
  *         channels] float32: the states before every 8th token of each sequence,
- *         which ssd_selective_scan_bwd reads (entries of no sequence stay unwritten)
+ *         which ssd_selective_scan_bwd reads (entries of no sequence stay unwritten).
+ *         That is dstate / 2 bytes per token and channel: 8 at 16 states, four times a
+ *         bfloat16 activation, and 32 at 64 states
  *  y      [tokens, channels] io_dtype, contiguous
  */
 size_t ssd_selective_scan_chunk_states(int tokens, int nseq);

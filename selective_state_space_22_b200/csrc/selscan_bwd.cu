@@ -18,9 +18,10 @@
 // the block's warps in shared memory, and over blocks by sel_bwd_sum, all in a fixed
 // order.  Bound by issue and latency: the registers of a half (step, input and upstream
 // gradient of 4 tokens, three sums for each, a_t and h_{t-1}) leave 16 warps to an SM.
-// Measured at 64 x 512 tokens, 1024 channels, 16 states, bf16: 990 us.  A form that split a
-// chunk's tokens over the lanes of a warp took 1428 us, one with a channel per thread and
-// its states paired 1490 us (each step, input and gradient held twice, spilled).
+// Measured at 64 x 512 tokens, 1024 channels, 16 states, bf16: 1090 us, issue slots 53 % busy.
+// Before the sums over channels took each product in two parts it was 990 us; then a form
+// that split a chunk's tokens over the lanes of a warp took 1428 us, one with a channel per
+// thread and its states paired 1490 us (each step, input and gradient held twice, spilled).
 #include "selscan_seg.cuh"
 
 namespace ssd {
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, BWD_BLOCKS_PER_SM) sel_bwd_kerne
         // a[k] = exp(delta_k A). Decays near one, where the whole warp has them, by the
         // polynomial: the gradient of the state adds up many of their errors (dA 1.2e-6 off
         // with the approximate exponential everywhere, 6.3e-7 so, at 32 sequences of 512
-        // tokens; 64 of them take 907 and 990 us). The state before a second half is four
+        // tokens; 64 of them took 907 us so, 990 us with it). The state before a second half is four
         // tokens away from one that was kept, and does without.
         auto decays = [&](float2 A2, float2 (&a)[SUB]) {
             if (__all_sync(0xffffffffu, most * fmaxf(fabsf(A2.x), fabsf(A2.y)) <= SMALL_EXP)) {

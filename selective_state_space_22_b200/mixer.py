@@ -10,6 +10,11 @@ projection's output holds side by side may be passed as slices: rows may be
 strided, the last dimension may not.  Outputs and scratch are allocated for each
 call on the stream that the call runs on, so calls on several streams and captured
 graphs never share scratch.
+
+No call records an autograd graph: a result carries no gradient even where an input
+requires one.  Training calls the ``_bwd`` functions, or wraps a pair in its own
+torch.autograd.Function.  A dict given as ``out`` may be an earlier call's: what it
+holds is written again, and gradients of absent inputs become None.
 """
 from __future__ import annotations
 
@@ -122,7 +127,8 @@ def ssd_selective_scan_varlen(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bia
     int32.  dt is before the bias and the softplus.  state [nslots, channels, N]
     float32 is read where has_init (bool [nseq]) says so and left holding each
     prompt's end state, in slot slots[i] (int32; None: i).  return_chunk_states keeps
-    what ssd_selective_scan_bwd needs."""
+    what ssd_selective_scan_bwd needs: N / 2 bytes per token and channel (268 MB for
+    32768 tokens of 1024 channels of 16 states)."""
     return _run("selective_scan_varlen", stream, x, dt, A, B, C, D, z, dt_bias, softplus, cu_seqlens, state, slots,
                 has_init, y, return_chunk_states)
 
