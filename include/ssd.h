@@ -529,7 +529,8 @@ ssd_status ssd_residual_rmsnorm(const void *x, long long x_stride, const void *r
  * it), dout the gradient at out, dresidual the one at residual_out (residual_dtype,
  * or NULL for none).  Outputs: dresidual_in (residual_dtype) and dx (io_dtype),
  * either may be NULL; dweight; and with scale given, which needs x, dscale.
- * dresidual_in may be dresidual itself.  Two launches.
+ * dresidual_in may be dresidual itself, and dx too where neither scale nor
+ * residual_dtype sets the two apart.  Two launches.
  */
 size_t ssd_rmsnorm_bwd_workspace_size(int rows, int width);
 ssd_status ssd_residual_rmsnorm_bwd(const void *residual, long long residual_stride,

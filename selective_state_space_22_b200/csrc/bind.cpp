@@ -474,7 +474,8 @@ PyObject *residual_rmsnorm_bwd(PyObject *const *a) {
         given = PyDict_GetItemString(out.d, "dx");
     }
     const Tensor gx = apart || !none(given) ? out.tensor_of(c, "dx", type, shape) : Tensor();
-    if (apart && overlap(gx, gr)) throw Refused("out: dx and dresidual share memory, and scale or the residual's dtype sets them apart");
+    if (gx.defined() && overlap(gx, gr) && (apart || ptr(gx) != ptr(gr)))
+        throw Refused("out: dx and dresidual share memory and are not the same values at the same place");
     if (!gx.defined()) out.set("dx", wrap(gr));
     const Tensor gw = out.tensor_of(c, "dweight", at::kFloat, {d}), gs = scaled ? out.tensor_of(c, "dscale", at::kFloat, {d}) : Tensor();
     if (!scaled) out.absent("dscale");

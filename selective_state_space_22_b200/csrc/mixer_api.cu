@@ -408,6 +408,8 @@ ssd_status ssd_residual_rmsnorm_bwd(const void *residual, long long residual_str
         NEED(dout);
         if (scale) NEED(x);
         if (!dx && !dresidual_in) return refuse(SSD_ERR_INVALID_ARG, "dx or dresidual_in must be non-null");
+        if (dx && dx == dresidual_in && (scale || residual_dtype != io_dtype))
+            return refuse(SSD_ERR_INVALID_ARG, "dx and dresidual_in are one array, and scale or residual_dtype sets them apart");
         NEED_STRIDE(residual_stride, width);
         if (scale) NEED_STRIDE(x_stride, width);
     }

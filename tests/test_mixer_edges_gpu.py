@@ -43,6 +43,8 @@ def test_scaled_norm_gradient_into_the_dict_of_an_unscaled_call():
     for a, b in ((both[:n], both[:n]), (both[:n], both[1:])):
         with pytest.raises(ValueError, match="share memory"):
             ssd.ssd_residual_rmsnorm_bwd(r, w, dout, up, x, s, out=dict(dx=a, dresidual=b))
+    with pytest.raises(ValueError, match="share memory"):  # rows that lie a row apart
+        ssd.ssd_residual_rmsnorm_bwd(r, w, dout, up, out=dict(dx=both[:n], dresidual=both[1:]))
     for _ in range(2):  # without scale one tensor for both stays what it was
         again = ssd.ssd_residual_rmsnorm_bwd(r, w, dout, up, out=dict(dx=first, dresidual=first))
         assert again["dx"] is first and again["dresidual"] is first and torch.equal(first, want["dresidual"])
@@ -99,11 +101,12 @@ def test_gradients_of_b_and_c_where_channels_cancel(io, d, G, N, lens):
         assert (got[k] == per // 2).all(), (k, got[k].flatten()[:4])
 
 
+@pytest.mark.parametrize("full", [False, True])
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("d,G,N", [(40, 1, 4), (66, 2, 8), (33, 1, 16), (36, 1, 7), (70, 1, 32), (40, 2, 64)])
 @pytest.mark.parametrize("lens,t0", [([5, 30], 17), ([35], 18), ([35], 34), ([6, 2, 27], 7), ([75], 42)])
-def test_an_infinity_reaches_the_gradients_that_have_it_in_their_sums_and_no_other(io, d, G, N, lens, t0):
-    """One infinite x, dy or z of a channel: B's and C's gradients of the other tokens, groups
+def test_an_infinity_reaches_the_gradients_that_have_it_in_their_sums_and_no_other(io, d, G, N, lens, t0, full):
+    """One infinite x or dy of a channel: B's and C's gradients of the other tokens, groups
     and states, and the other channels' gradients, are what the formulas say.  Decays are mild
     and every input is away from zero, so that no 0 * infinity arises in the formulas but in
     what is infinite anyway."""
@@ -113,13 +116,16 @@ def test_an_infinity_reaches_the_gradients_that_have_it_in_their_sums_and_no_oth
     for where in ("x", "dy"):
         x, dt, B, C, dy = mk(d), mk(d) * 0.1, mk(G, N), mk(G, N), mk(d)
         (x if where == "x" else dy)[t0, c0] = float("inf")
-        want = ref.sel_bwd(d64(x), d64(dt), d64(A), d64(B), d64(C), cu, d64(dy), softplus=False)
-        _, kept = ssd.ssd_selective_scan_varlen(x, dt, A, B, C, cu, softplus=False, return_chunk_states=True)
-        got = ssd.ssd_selective_scan_bwd(x, dt, A, B, C, cu, dy, kept, softplus=False)
+        opt = (mk(d)[0].float().contiguous(), mk(d), -mk(d)[0].float() - 1) if full else (None,) * 3
+        want = ref.sel_bwd(d64(x), d64(dt), d64(A), d64(B), d64(C), cu, d64(dy), *map(d64, opt), softplus=full)
+        _, kept = ssd.ssd_selective_scan_varlen(x, dt, A, B, C, cu, *opt, softplus=full, return_chunk_states=True)
+        got = ssd.ssd_selective_scan_bwd(x, dt, A, B, C, cu, dy, kept, *opt, softplus=full)
         ssd.ssd_get_device_status()
-        r = 2 * sel_roundings(max(lens), N, (x, dt, A), (None,) * 3, False) + d
-        for k in ("dx", "ddt", "dA", "dB", "dC"):
-            v, m = want[k]
+        r = 2 * sel_roundings(max(lens), N, (x, dt, A), opt, full) + d
+        for k, (v, m) in want.items():
+            if got[k] is None:
+                assert not full and k in ("dD", "dz", "ddt_bias")
+                continue
             assert torch.equal(torch.isfinite(d64(got[k])), torch.isfinite(v)), (where, k)
             close(got[k], v, m, r + n, k, torch.isfinite(v))
 

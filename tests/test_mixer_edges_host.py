@@ -24,6 +24,17 @@ def test_slots_of_a_conv_without_states_are_checked_too(lib):
     assert update(FAKE, 2) == ssd.SSD_ERR_INVALID_ARG and "conv_state" in ssd.ssd_last_error()  # two taps need one
 
 
+def test_one_array_for_two_different_gradients_is_refused(lib):
+    def bwd(io, rio, scale, dx, dres):
+        s = FAKE if scale else None
+        return lib.ssd_residual_rmsnorm_bwd(FAKE, 8, FAKE, FAKE, None, s, 8, s, dx, dres, FAKE, s, io, rio, 4, 8, 1e-5, None, 0, None)
+
+    for io, rio, scale in ((0, 0, True), (1, 0, False), (1, 1, True)):
+        assert bwd(io, rio, scale, FAKE, FAKE) == ssd.SSD_ERR_INVALID_ARG and "one array" in ssd.ssd_last_error()
+        assert bwd(io, rio, scale, FAKE, FAKE + 4096) == ssd.SSD_ERR_WORKSPACE  # the next check
+    assert bwd(0, 0, False, FAKE, FAKE) == ssd.SSD_ERR_WORKSPACE
+
+
 def test_a_stream_of_another_device_is_refused():
     """It would be replaced by the tensors' device's own stream, which nobody waits for."""
     at = lambda k: types.SimpleNamespace(device=torch.device("cuda", k))  # noqa: E731
