@@ -536,6 +536,12 @@ PyObject *gated_rmsnorm_bwd(PyObject *const *a) {
 }
 
 // ----------------------------------------------------------------------- module
+void set_error(const char *module, const char *type, const char *what) {
+    PyObject *m = PyImport_ImportModule(module), *t = m ? PyObject_GetAttrString(m, type) : nullptr;
+    if (t) PyErr_SetString(t, what);
+    Py_XDECREF(t);
+    Py_XDECREF(m);
+}
 template <PyObject *(*F)(PyObject *const *), int N> PyObject *guarded(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != N) {
         PyErr_Format(PyExc_TypeError, "%d arguments expected, got %zd", N, n);
@@ -547,7 +553,7 @@ template <PyObject *(*F)(PyObject *const *), int N> PyObject *guarded(PyObject *
         PyErr_SetString(PyExc_ValueError, e.what());
     } catch (const PythonError &) {
     } catch (const c10::OutOfMemoryError &e) {
-        PyErr_SetString(PyExc_MemoryError, e.what());
+        set_error("torch", "OutOfMemoryError", e.what_without_backtrace());
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     }

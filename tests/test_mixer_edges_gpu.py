@@ -288,3 +288,17 @@ def test_bad_bounds_do_not_hide_a_timeout():
                 ssd.ssd_get_device_status()
             assert e.value.status == status
         ssd.ssd_get_device_status()
+
+
+def test_no_memory_is_torchs_error():
+    """Kept states for 2^24 empty prompts of 64 channels and states (275 GB) cannot be had:
+    the allocator's own error, as from any other call, and the next call runs."""
+    g, d, N = gen(88), 64, 64
+    (x, dt, A, B, C), _ = sel_inputs(g, 3, d, 1, N, torch.bfloat16, 0)
+    cu = torch.zeros((1 << 24) + 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        ssd.ssd_selective_scan_varlen(x, dt, A, B, C, cu, return_chunk_states=True)
+    del cu
+    y, kept = ssd.ssd_selective_scan_varlen(x, dt, A, B, C, bounds([3]), return_chunk_states=True)
+    ssd.ssd_get_device_status()
+    assert kept.shape == (1, N, d) and torch.isfinite(y).all()
